@@ -50,6 +50,11 @@ EXPORTS = (
     "sambay_decode_step",
     "sambay_cross_attn_decode_workspace",
     "sambay_cross_attn_decode",
+    "sambay_kv4_cache_bytes",
+    "sambay_kv4_write",
+    "sambay_kv4_read",
+    "sambay_cross_attn_decode_kv4_workspace",
+    "sambay_cross_attn_decode_kv4",
     "sambay_ssd_prefill_workspace",
     "sambay_ssd_prefill",
     "sambay_ssd_step_workspace",
@@ -104,6 +109,29 @@ class AttnDims(ctypes.Structure):
     ]
 
 
+class Kv4Dims(ctypes.Structure):
+    """sambay_kv4_dims: the sizes of a 4-bit KV cache in pages."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("table_pages", ctypes.c_int32),
+        ("io", ctypes.c_int32),
+    ]
+
+
+class Kv4Cache(ctypes.Structure):
+    """sambay_kv4_cache: a 4-bit KV cache's device pointers."""
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("k_exp", ctypes.c_void_p),
+        ("v_exp", ctypes.c_void_p),
+    ]
+
+
 class SsdDims(ctypes.Structure):
     """sambay_ssd_dims: the SambaY-2 (Mamba-2) layer's sizes."""
     _fields_ = [
@@ -152,6 +180,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     pg = ctypes.POINTER(GmuWeights)
     pa = ctypes.POINTER(AttnDims)
     psd, psw = ctypes.POINTER(SsdDims), ctypes.POINTER(SsdWeights)
+    pkd, pkc = ctypes.POINTER(Kv4Dims), ctypes.POINTER(Kv4Cache)
     sig = {
         "sambay_scan_prefill_workspace": (sz, [pd]),
         "sambay_scan_step_workspace": (sz, [pd]),
@@ -173,6 +202,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sambay_decode_step_workspace": (sz, [pd, i32]),
         "sambay_cross_attn_decode_workspace": (sz, [pa]),
         "sambay_cross_attn_decode": (ctypes.c_int, [pa, vp, vp, vp, vp, ctypes.c_float, vp, sz, vp]),
+        "sambay_kv4_cache_bytes": (sz, [pkd]),
+        "sambay_kv4_write": (ctypes.c_int, [pkc, pkd, i32, vp, vp, i64, i64, vp, vp, vp]),
+        "sambay_kv4_read": (ctypes.c_int, [pkc, pkd, i32, vp, vp, vp, vp, vp]),
+        "sambay_cross_attn_decode_kv4_workspace": (sz, [pkd, i32, i32]),
+        "sambay_cross_attn_decode_kv4": (ctypes.c_int, [pkc, pkd, i32, i32, vp, vp, vp, vp, ctypes.c_float, vp, sz, vp]),
         "sambay_ssd_prefill_workspace": (sz, [psd]),
         "sambay_ssd_prefill": (ctypes.c_int, [psw, psd, vp, vp, vp, vp, vp, i32, vp, sz, vp]),
         "sambay_ssd_step_workspace": (sz, [psd]),
@@ -299,6 +333,38 @@ def sambay_cross_attn_decode(dims: AttnDims, q, K, V, out, scale: float, ws, str
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check("sambay_cross_attn_decode", load().sambay_cross_attn_decode(
         ctypes.byref(dims), _p(q), _p(K), _p(V), _p(out), scale, _p(ws), ws_bytes, _stream(stream)))
+
+
+def make_kv4_cache(pages, table, k_exp=None, v_exp=None) -> Kv4Cache:
+    return Kv4Cache(*(None if t is None else t.data_ptr() for t in (pages, table, k_exp, v_exp)))
+
+
+def sambay_kv4_cache_bytes(dims: Kv4Dims) -> int:
+    return load().sambay_kv4_cache_bytes(ctypes.byref(dims))
+
+
+def sambay_kv4_write(cache: Kv4Cache, dims: Kv4Dims, tokens: int, K, V, pos, count=None, k_stride: int = 0,
+                     v_stride: int = 0, stream=None):
+    _check("sambay_kv4_write", load().sambay_kv4_write(
+        ctypes.byref(cache), ctypes.byref(dims), tokens, _p(K), _p(V), k_stride, v_stride, _p(pos), _p(count),
+        _stream(stream)))
+
+
+def sambay_kv4_read(cache: Kv4Cache, dims: Kv4Dims, tokens: int, K, V, pos, count=None, stream=None):
+    _check("sambay_kv4_read", load().sambay_kv4_read(
+        ctypes.byref(cache), ctypes.byref(dims), tokens, _p(K), _p(V), _p(pos), _p(count), _stream(stream)))
+
+
+def sambay_cross_attn_decode_kv4_workspace(dims: Kv4Dims, q_heads: int, tokens: int) -> int:
+    return load().sambay_cross_attn_decode_kv4_workspace(ctypes.byref(dims), q_heads, tokens)
+
+
+def sambay_cross_attn_decode_kv4(cache: Kv4Cache, dims: Kv4Dims, q_heads: int, tokens: int, q, out, lens, count,
+                                 scale: float, ws, stream=None):
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check("sambay_cross_attn_decode_kv4", load().sambay_cross_attn_decode_kv4(
+        ctypes.byref(cache), ctypes.byref(dims), q_heads, tokens, _p(q), _p(out), _p(lens), _p(count), scale, _p(ws),
+        ws_bytes, _stream(stream)))
 
 
 def sambay_ssd_prefill_workspace(dims: SsdDims) -> int:

@@ -1,7 +1,8 @@
 // libsambay: C ABI of the SambaY scan + Gated Memory Unit hot path on B200.
 // Host side: argument validation, workspace carving, TMA descriptors and
 // kernel launches.  Every step of the computation runs in the kernels of
-// scan_kernels.cuh, step_kernels.cuh, tc_gemm.cuh and simt_gemm.cuh.
+// scan_kernels.cuh, step_kernels.cuh, tc_gemm.cuh, simt_gemm.cuh,
+// attn_kernels.cuh, kv4_kernels.cuh and ssd_kernels.cuh.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -18,6 +19,7 @@
 #include "../../include/sambay.h"
 #include "common.cuh"
 #include "attn_kernels.cuh"
+#include "kv4_kernels.cuh"
 #include "scan_kernels.cuh"
 #include "simt_gemm.cuh"
 #include "ssd_kernels.cuh"
@@ -1580,6 +1582,237 @@ sambay_status sambay_cross_attn_decode(const sambay_attn_dims* a, const void* q,
   p.scale_log2 = sc * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return a->head_dim == 64 ? attn_launch<64>(dev, sms, p, st) : attn_launch<128>(dev, sms, p, st);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ the KV cache in 4 bits
+
+namespace {
+
+sambay_status kv4_check(const sambay_kv4_dims* d) {
+  if (!d) return SAMBAY_ERR_INVALID_ARG;
+  if (d->batch < 1 || d->kv_heads < 1 || d->head_dim < 1 || d->page_tokens < 1 || d->num_pages < 1 ||
+      d->table_pages < 1)
+    return SAMBAY_ERR_INVALID_ARG;
+  if (d->io != SAMBAY_F32 && d->io != SAMBAY_BF16) return SAMBAY_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return SAMBAY_ERR_UNSUPPORTED;
+  if (d->page_tokens < 16 || d->page_tokens > 1024 || (d->page_tokens & (d->page_tokens - 1)) != 0)
+    return SAMBAY_ERR_UNSUPPORTED;
+  if (static_cast<long long>(d->table_pages) * d->page_tokens > (1LL << 30)) return SAMBAY_ERR_UNSUPPORTED;
+  if (d->kv_heads > 65535 || d->batch > 65535) return SAMBAY_ERR_UNSUPPORTED;
+  return SAMBAY_OK;
+}
+
+sambay_status kv4_check_index(const void* p, bool optional) {
+  if (!p) return optional ? SAMBAY_OK : SAMBAY_ERR_INVALID_ARG;
+  return (reinterpret_cast<uintptr_t>(p) & 3u) ? SAMBAY_ERR_UNSUPPORTED : SAMBAY_OK;
+}
+
+sambay_status kv4_check_cache(const sambay_kv4_cache* c) {
+  if (!c) return SAMBAY_ERR_INVALID_ARG;
+  SAMBAY_TRY(check_ptrs({c->pages}));
+  SAMBAY_TRY(kv4_check_index(c->table, false));
+  SAMBAY_TRY(kv4_check_index(c->k_exp, true));
+  return kv4_check_index(c->v_exp, true);
+}
+
+sambay::kv4::Pages kv4_pages(const sambay_kv4_cache* c, const sambay_kv4_dims* d) {
+  sambay::kv4::Pages pg{};
+  pg.cache = static_cast<uint8_t*>(c->pages);
+  pg.table = c->table;
+  pg.k_exp = c->k_exp;
+  pg.v_exp = c->v_exp;
+  pg.B = d->batch;
+  pg.Hkv = d->kv_heads;
+  pg.page_log2 = 0;
+  while ((1 << pg.page_log2) < d->page_tokens) ++pg.page_log2;
+  pg.num_pages = d->num_pages;
+  pg.table_pages = d->table_pages;
+  return pg;
+}
+
+// Rows of a write or read: B * tokens * Hkv of them, 32 a CTA.
+sambay_status kv4_check_rows(const sambay_kv4_dims* d, int32_t tokens) {
+  if (tokens < 1) return SAMBAY_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(d->batch) * tokens;
+  if (rows > (1LL << 36) / d->kv_heads) return SAMBAY_ERR_UNSUPPORTED;
+  return SAMBAY_OK;
+}
+
+template <typename T, int D>
+sambay_status kv4_rows_launch(bool write, const sambay::kv4::RowParams<T>& p, cudaStream_t st) {
+  const long long units = static_cast<long long>(p.pg.B) * p.T_ * p.pg.Hkv;
+  auto kern = write ? sambay::kv4::kv4_write_kernel<T, D> : sambay::kv4::kv4_read_kernel<T, D>;
+  ProfScope ps(write ? "kv4_write" : "kv4_read", st);
+  return launch_k(kern, dim3(static_cast<unsigned>((units + 31) / 32)), dim3(256), 0, st, false, 1, p) == cudaSuccess
+             ? SAMBAY_OK
+             : SAMBAY_ERR_CUDA;
+}
+
+template <typename T>
+sambay_status kv4_rows(bool write, const sambay_kv4_cache* c, const sambay_kv4_dims* d, int32_t tokens, const void* K,
+                       const void* V, int64_t k_stride, int64_t v_stride, const int32_t* pos, const int32_t* count,
+                       cudaStream_t st) {
+  sambay::kv4::RowParams<T> p{};
+  p.pg = kv4_pages(c, d);
+  p.K = static_cast<const T*>(K);
+  p.V = static_cast<const T*>(V);
+  p.Ko = static_cast<T*>(const_cast<void*>(K));
+  p.Vo = static_cast<T*>(const_cast<void*>(V));
+  p.pos = pos;
+  p.count = count;
+  p.T_ = tokens;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  return d->head_dim == 64 ? kv4_rows_launch<T, 64>(write, p, st) : kv4_rows_launch<T, 128>(write, p, st);
+}
+
+constexpr int kKv4MaxTokens = 16;
+
+// Split-KV plan of the attention: enough (row tile, KV head, sequence, split)
+// CTAs to cover a 148-SM B200 about three times (a function of the sizes only).
+struct Kv4Plan {
+  int nt = 1, row_tiles = 1, splits = 1;
+  size_t o_part = 0, ml_part = 0, total = 0;
+};
+
+Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
+  Kv4Plan pl;
+  const int rows = q_heads / d->kv_heads * tokens;
+  pl.nt = rows <= 8 ? 1 : 2;
+  pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
+  const long long ctas = static_cast<long long>(d->batch) * d->kv_heads * pl.row_tiles;
+  constexpr int kBlock = sambay::kv4::kTile * sambay::kv4::kWarps;
+  const long long blocks = (static_cast<long long>(d->table_pages) * d->page_tokens + kBlock - 1) / kBlock;
+  pl.splits = static_cast<int>(std::min(blocks, std::max(1LL, (3LL * kSplitTarget + ctas - 1) / ctas)));
+  if (pl.splits > 1) {
+    const size_t cols = static_cast<size_t>(ctas) * pl.splits * 8 * pl.nt;
+    pl.ml_part = round256(cols * d->head_dim * 4);
+    pl.total = pl.ml_part + round256(cols * 2 * 4);
+  }
+  return pl;
+}
+
+template <typename T, int D, int NT>
+sambay_status kv4_attn_launch(const sambay::kv4::AttnParams& p, cudaStream_t st) {
+  using namespace sambay::kv4;
+  {
+    ProfScope ps("kv4_attn", st);
+    if (launch_k(kv4_attn_kernel<T, D, NT, sizeof(T) == 4>, dim3(p.splits * p.row_tiles, p.pg.Hkv, p.pg.B),
+                 dim3(kThreads), 0, st, false, 1, p) != cudaSuccess)
+      return SAMBAY_ERR_CUDA;
+  }
+  if (p.splits > 1) {
+    const long long n = static_cast<long long>(p.pg.B) * p.T_ * p.Hq * D;
+    ProfScope ps("kv4_combine", st);
+    if (launch_k(kv4_combine_kernel<T, D, NT>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st, true,
+                 1, p) != cudaSuccess)
+      return SAMBAY_ERR_CUDA;
+  }
+  return SAMBAY_OK;
+}
+
+template <typename T>
+sambay_status kv4_attn(const sambay::kv4::AttnParams& p, int dh, int nt, cudaStream_t st) {
+  if (dh == 64) return nt == 1 ? kv4_attn_launch<T, 64, 1>(p, st) : kv4_attn_launch<T, 64, 2>(p, st);
+  return nt == 1 ? kv4_attn_launch<T, 128, 1>(p, st) : kv4_attn_launch<T, 128, 2>(p, st);
+}
+
+sambay_status kv4_attn_check(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
+  SAMBAY_TRY(kv4_check(d));
+  if (q_heads < 1 || tokens < 1) return SAMBAY_ERR_INVALID_ARG;
+  if (q_heads % d->kv_heads != 0 || q_heads / d->kv_heads > 16 || tokens > kKv4MaxTokens)
+    return SAMBAY_ERR_UNSUPPORTED;
+  return SAMBAY_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sambay_kv4_cache_bytes(const sambay_kv4_dims* d) {
+  if (kv4_check(d) != SAMBAY_OK) return 0;
+  return static_cast<size_t>(d->num_pages) * d->kv_heads * (d->page_tokens / 16) * 18 * d->head_dim;
+}
+
+sambay_status sambay_kv4_write(const sambay_kv4_cache* c, const sambay_kv4_dims* d, int32_t tokens, const void* K,
+                               const void* V, int64_t k_stride, int64_t v_stride, const int32_t* pos,
+                               const int32_t* count, sambay_stream_t stream) {
+  SAMBAY_TRY(kv4_check(d));
+  SAMBAY_TRY(kv4_check_cache(c));
+  SAMBAY_TRY(kv4_check_rows(d, tokens));
+  SAMBAY_TRY(check_ptrs({K, V}));
+  SAMBAY_TRY(kv4_check_index(pos, false));
+  SAMBAY_TRY(kv4_check_index(count, true));
+  const int64_t dense = static_cast<int64_t>(d->kv_heads) * d->head_dim;
+  const int64_t per16 = 16 / static_cast<int64_t>(io_bytes(d->io));
+  for (int64_t* s : {&k_stride, &v_stride}) {
+    if (*s == 0) *s = dense;
+    if (*s < dense) return SAMBAY_ERR_INVALID_ARG;
+    if (*s % per16 != 0 || *s > (1LL << 40)) return SAMBAY_ERR_UNSUPPORTED;
+  }
+  if (K == c->pages || V == c->pages) return SAMBAY_ERR_INVALID_ARG;
+  int dev, sms;
+  SAMBAY_TRY(current_device(&dev, &sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return d->io == SAMBAY_BF16 ? kv4_rows<bf16>(true, c, d, tokens, K, V, k_stride, v_stride, pos, count, st)
+                              : kv4_rows<float>(true, c, d, tokens, K, V, k_stride, v_stride, pos, count, st);
+}
+
+sambay_status sambay_kv4_read(const sambay_kv4_cache* c, const sambay_kv4_dims* d, int32_t tokens, void* K, void* V,
+                              const int32_t* pos, const int32_t* count, sambay_stream_t stream) {
+  SAMBAY_TRY(kv4_check(d));
+  SAMBAY_TRY(kv4_check_cache(c));
+  SAMBAY_TRY(kv4_check_rows(d, tokens));
+  SAMBAY_TRY(check_ptrs({K, V}));
+  SAMBAY_TRY(kv4_check_index(pos, false));
+  SAMBAY_TRY(kv4_check_index(count, true));
+  if (K == V || K == c->pages || V == c->pages) return SAMBAY_ERR_INVALID_ARG;
+  int dev, sms;
+  SAMBAY_TRY(current_device(&dev, &sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return d->io == SAMBAY_BF16 ? kv4_rows<bf16>(false, c, d, tokens, K, V, 0, 0, pos, count, st)
+                              : kv4_rows<float>(false, c, d, tokens, K, V, 0, 0, pos, count, st);
+}
+
+size_t sambay_cross_attn_decode_kv4_workspace(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
+  if (kv4_attn_check(d, q_heads, tokens) != SAMBAY_OK) return 0;
+  return kv4_plan(d, q_heads, tokens).total;
+}
+
+sambay_status sambay_cross_attn_decode_kv4(const sambay_kv4_cache* c, const sambay_kv4_dims* d, int32_t q_heads,
+                                           int32_t tokens, const void* q, void* out, const int32_t* lens,
+                                           const int32_t* count, float scale, void* ws, size_t ws_bytes,
+                                           sambay_stream_t stream) {
+  SAMBAY_TRY(kv4_attn_check(d, q_heads, tokens));
+  SAMBAY_TRY(kv4_check_cache(c));
+  SAMBAY_TRY(check_ptrs({q, out}));
+  SAMBAY_TRY(kv4_check_index(lens, false));
+  SAMBAY_TRY(kv4_check_index(count, true));
+  if (out == q || out == c->pages || q == c->pages) return SAMBAY_ERR_INVALID_ARG;
+  if (!(scale >= 0.0f) || scale > 1e4f) return SAMBAY_ERR_INVALID_ARG;   // also rejects NaN
+  const Kv4Plan pl = kv4_plan(d, q_heads, tokens);
+  SAMBAY_TRY(check_ws(ws, ws_bytes, pl.total));
+  int dev, sms;
+  SAMBAY_TRY(current_device(&dev, &sms));
+  sambay::kv4::AttnParams p{};
+  p.pg = kv4_pages(c, d);
+  p.q = q;
+  p.out = out;
+  p.lens = lens;
+  p.count = count;
+  p.o_part = pl.splits > 1 ? static_cast<float*>(ws) : nullptr;
+  p.ml_part = pl.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.ml_part) : nullptr;
+  p.T_ = tokens;
+  p.Hq = q_heads;
+  p.G = q_heads / d->kv_heads;
+  p.splits = pl.splits;
+  p.row_tiles = pl.row_tiles;
+  const float sc = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d->head_dim));
+  p.scale_log2 = sc * sambay::kLog2e;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return d->io == SAMBAY_BF16 ? kv4_attn<bf16>(p, d->head_dim, pl.nt, st) : kv4_attn<float>(p, d->head_dim, pl.nt, st);
 }
 
 // ------------------------------------------------------------ SambaY-2 (Mamba-2 SSD)

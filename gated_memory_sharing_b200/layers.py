@@ -289,3 +289,152 @@ class Mamba2Scan:
             self._ws[("step", B)] = ws
         abi.sambay_ssd_step(self.abi_w, d, xbc_t, dt_raw_t, m_t, ssm_state, conv_state, ws, stream)
         return m_t
+
+
+class KV4Cache:
+    """The one KV cache of the cross-decoder in 4 bits: rows are quantised as
+    they are written (4.5 bits an element), read back, and attended over.
+
+    Pages of ``page_tokens`` tokens from a pool of ``num_pages``; ``table``
+    [B, pages a sequence] int32 says which page holds which tokens (by default
+    each sequence has its own pages, in order).  The table may be changed in
+    place between calls, on the stream of the calls.  ``k_exp`` / ``v_exp``
+    [Hkv] int32: the power of two of each head's rows (see :meth:`exponents`),
+    fixed for the cache's life.
+
+    Positions, lengths and counts are int32 tensors on the device.  Indices
+    outside the table, the pool or a call's rows are skipped and recorded
+    (``abi.sambay_device_status``).  Workspaces come from torch's allocator
+    call by call, so calls on different streams and captured graphs share none.
+    """
+
+    def __init__(self, batch: int, kv_heads: int, head_dim: int, max_tokens: int, page_tokens: int = 64,
+                 io: int = abi.BF16, num_pages=None, table=None, k_exp=None, v_exp=None, device="cuda"):
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        each = -(-max_tokens // page_tokens)
+        if table is None:
+            if num_pages is None:
+                num_pages = batch * each
+            if num_pages < batch * each:
+                raise ValueError(f"{num_pages} pages are not enough for {batch} sequences of {each} pages: give a table")
+            table = torch.arange(batch * each, dtype=torch.int32, device=self.device).view(batch, each)
+        elif num_pages is None:
+            raise ValueError("a table needs num_pages, the pool's size")
+        self.io, self.dtype = io, io_dtype(io)
+        self.batch, self.kv_heads, self.head_dim, self.page_tokens = batch, kv_heads, head_dim, page_tokens
+        self.table, self.k_exp, self.v_exp = table, k_exp, v_exp
+        if table.dim() != 2 or table.shape[0] != batch:
+            raise ValueError(f"table is [{batch}, pages]: got {tuple(table.shape)}")
+        self._index(table, "table", None)
+        for name, e in (("k_exp", k_exp), ("v_exp", v_exp)):
+            if e is not None:
+                self._index(e, name, kv_heads)
+        self.dims = abi.Kv4Dims(batch, kv_heads, head_dim, page_tokens, num_pages, table.shape[1], io)
+        nbytes = abi.sambay_kv4_cache_bytes(self.dims)
+        if nbytes == 0:
+            raise ValueError("unsupported sizes: head_dim 64 or 128, page_tokens a power of two in 16 .. 1024, "
+                             "at most 2^30 tokens a sequence")
+        with torch.cuda.device(self.device):
+            # zeros: a page that was never written reads as zeros
+            self.pages = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.abi_cache = abi.make_kv4_cache(self.pages, table, k_exp, v_exp)
+        self._ws_bytes = {}
+
+    @staticmethod
+    def exponents(rows) -> torch.Tensor:
+        """[Hkv] int32 for rows [..., Hkv, dh]: the least e for which the
+        largest of these values is not past what a block can hold, 2688 * 2^e."""
+        amax = rows.detach().abs().amax(-1).reshape(-1, rows.shape[-2]).amax(0).double()
+        e = torch.ceil(torch.log2(torch.clamp(amax, min=2.0 ** -60) / 2688.0))
+        return torch.clamp(e, -64, 64).to(torch.int32)
+
+    # ------------------------------------------------------------- checks
+
+    def _index(self, t, name, n):
+        if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or (n is not None and t.numel() != n):
+            raise ValueError(f"{name}: {'an' if n is None else n} int32 dense on {self.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+    def _rows(self, t, name, shape, dense=True):
+        if t.dtype != self.dtype or t.device != self.device or t.shape != shape:
+            raise ValueError(f"{name}: {self.dtype} {tuple(shape)} on {self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        if dense and not t.is_contiguous():
+            raise ValueError(f"{name} must be dense")
+
+    def _stride(self, t, name):
+        """Elements between a sequence's consecutive tokens; heads and values
+        are dense and sequences follow at the same stride."""
+        B, T, H, D = t.shape
+        s = t.stride()
+        token = s[1] if T > 1 else s[0] if B > 1 else H * D
+        if s[3] != 1 or (H > 1 and s[2] != D) or (B > 1 and s[0] != T * token):
+            raise ValueError(f"{name}: strides {s} are not [tokens * stride, stride, {D}, 1]")
+        return token
+
+    def _device(self):
+        return torch.cuda.device(self.device)
+
+    # ------------------------------------------------------------- calls
+
+    def write(self, K, V, pos, count=None, stream=None):
+        """Quantise rows K, V [B, T, Hkv, dh] into positions pos[b] .. of each
+        sequence (count[b] of them, or all T).  Rows may be slices of wider
+        ones (a fused projection's)."""
+        shape = (self.batch, K.shape[1], self.kv_heads, self.head_dim)
+        self._rows(K, "K", shape, dense=False)
+        self._rows(V, "V", shape, dense=False)
+        ks, vs = self._stride(K, "K"), self._stride(V, "V")
+        self._index(pos, "pos", self.batch)
+        if count is not None:
+            self._index(count, "count", self.batch)
+        with self._device():
+            abi.sambay_kv4_write(self.abi_cache, self.dims, shape[1], K, V, pos, count, ks, vs, stream)
+
+    def read(self, pos, tokens: int, count=None, K=None, V=None, stream=None):
+        """The rows K, V [B, tokens, Hkv, dh] that positions pos[b] .. stand
+        for (count[b] of them, or all); rows from count[b] on are left as they
+        were (zeros in tensors made here)."""
+        shape = (self.batch, tokens, self.kv_heads, self.head_dim)
+        self._index(pos, "pos", self.batch)
+        if count is not None:
+            self._index(count, "count", self.batch)
+        with self._device():
+            K, V = (self._made(t, name, shape, stream, count is not None) for t, name in ((K, "K"), (V, "V")))
+            abi.sambay_kv4_read(self.abi_cache, self.dims, tokens, K, V, pos, count, stream)
+        return K, V
+
+    def attend(self, q, lens, count=None, scale: float = 0.0, out=None, stream=None):
+        """out [B, T, Hq, dh] for the queries q of the newest T (or count[b])
+        of each sequence's lens[b] cached tokens; q [B, Hq, dh] for one token
+        a sequence.  Rows from count[b] on are left as they were (zeros in a
+        tensor made here)."""
+        tokens = q.shape[1] if q.dim() == 4 else 1
+        heads = q.shape[-2]
+        shape = (self.batch, tokens, heads, self.head_dim) if q.dim() == 4 else (self.batch, heads, self.head_dim)
+        self._rows(q, "q", shape)
+        self._index(lens, "lens", self.batch)
+        if count is not None:
+            self._index(count, "count", self.batch)
+        n = self._ws_bytes.get((heads, tokens))
+        if n is None:
+            n = self._ws_bytes[(heads, tokens)] = abi.sambay_cross_attn_decode_kv4_workspace(self.dims, heads, tokens)
+        with self._device():
+            out = self._made(out, "out", shape, stream, count is not None)
+            ws = self._made(None, "ws", (n,), stream, False, torch.uint8) if n else None
+            abi.sambay_cross_attn_decode_kv4(self.abi_cache, self.dims, heads, tokens, q, out, lens, count, scale, ws,
+                                             stream)
+        return out
+
+    def _made(self, t, name, shape, stream, zero, dtype=None):
+        """`t`, checked; or a new tensor that the stream of the call owns."""
+        if t is not None:
+            self._rows(t, name, shape)
+            return t
+        make = torch.zeros if zero else torch.empty
+        if stream is None:
+            return make(shape, dtype=dtype or self.dtype, device=self.device)
+        on = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(on):
+            return make(shape, dtype=dtype or self.dtype, device=self.device)

@@ -37,8 +37,9 @@
  *     pointers, short workspace) are detected on the host BEFORE any launch,
  *     and return a status without touching the device.  Launch failures
  *     return SAMBAY_ERR_CUDA.  Faults found by a kernel while running (a
- *     bounded wait that ran out) are recorded in a per-device status word
- *     that sambay_device_status reads and clears.
+ *     bounded wait that ran out; an index outside the 4-bit cache) are
+ *     recorded in a per-device status word that sambay_device_status reads
+ *     and clears.
  *   - Supported sizes: d_state == 16, d_conv == 4, dt_rank a multiple of 4
  *     with dt_rank + 2*d_state <= 256, d_inner a multiple of 32 (scan) or 4
  *     (GMU), d_model a multiple of 4; in SAMBAY_BF16 mode d_inner and d_model
@@ -373,6 +374,104 @@ SAMBAY_API size_t sambay_cross_attn_decode_workspace(const sambay_attn_dims* dim
 SAMBAY_API sambay_status sambay_cross_attn_decode(const sambay_attn_dims* dims, const void* q,
                                                   const void* K, const void* V, void* out, float scale,
                                                   void* ws, size_t ws_bytes, sambay_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* The KV cache in 4 bits: written, read back, and attended over             */
+/* ---------------------------------------------------------------------- */
+
+/* Sizes of a 4-bit KV cache in pages. */
+typedef struct {
+  int32_t batch;        /* B sequences                                        */
+  int32_t kv_heads;     /* Hkv key/value heads                                */
+  int32_t head_dim;     /* dh: 64 or 128                                      */
+  int32_t page_tokens;  /* P tokens a page: a power of two, 16 .. 1024        */
+  int32_t num_pages;    /* pages of the pool                                  */
+  int32_t table_pages;  /* columns of the table: a sequence has room for
+                           table_pages * P tokens (at most 2^30)              */
+  int32_t io;           /* sambay_dtype of K, V, q and out                    */
+} sambay_kv4_dims;
+
+/* Device pointers. */
+typedef struct {
+  void* pages;            /* sambay_kv4_cache_bytes(dims) bytes, 16-byte aligned */
+  const int32_t* table;   /* [B, table_pages] the page that holds tokens
+                             j P .. j P + P - 1 of sequence b, at column j     */
+  const int32_t* k_exp;   /* [Hkv] e of K's rows, or NULL (0); clamped to
+                             -64 .. 64                                         */
+  const int32_t* v_exp;   /* [Hkv] e of V's rows, or NULL (0)                  */
+} sambay_kv4_cache;
+
+/*
+ * The 4-bit form of the one KV cache that the self-decoder's full-attention
+ * layer writes and every cross-attention layer reads [FRAME]; a cross-attention
+ * layer moves O(d_kv N) memory per decoded token, here 4.5 bits an element.
+ * Per token and head, each 16 values x of a row are kept as
+ *     x ~ 2^e s c,  s = e4m3(min(448, max|x| 2^-e / 6)),  c = e2m1(x 2^-e / s)
+ * (both to nearest even; |c| one of 0, .5, 1, 1.5, 2, 3, 4, 6).  e is fixed per
+ * head for the life of a cache (it brings the head's scales into e4m3's range,
+ * 2^-9 .. 448): the writer and every reader pass the same.  Larger values
+ * saturate at 2688 * 2^e.  A block holding a NaN or an infinity reads back as
+ * NaN.  What is kept is exact in float32 and bfloat16.  The order of the bytes
+ * inside a page is the library's own.
+ *
+ * Sequences may share pages that none of them writes.  The table, pos, count
+ * and lens are read on the device, when the call runs; a page outside the pool,
+ * a position outside the table or a count outside 0 .. tokens is skipped and
+ * recorded (sambay_device_status: SAMBAY_ERR_INVALID_ARG), the rest of the call
+ * completes.  int32 arrays are 4-byte aligned.
+ */
+SAMBAY_API size_t sambay_kv4_cache_bytes(const sambay_kv4_dims* dims);
+
+/*
+ * sambay_kv4_write - quantise K and V rows into the cache: row t of sequence b
+ * goes to position pos[b] + t, t < count[b] (a prompt's rows, or with tokens =
+ * 1 a decode step's).  Only the bytes of these positions change.
+ *
+ *   K, V   [B, tokens, Hkv, dh] io; heads and values dense, consecutive tokens
+ *          k_stride / v_stride elements apart (0: Hkv * dh; else at least that,
+ *          and whole 16 bytes), so slices of a fused projection's rows can be
+ *          passed; sequences tokens * stride apart.
+ *   pos    [B] int32;  count [B] int32 or NULL (all tokens).
+ */
+SAMBAY_API sambay_status sambay_kv4_write(const sambay_kv4_cache* cache, const sambay_kv4_dims* dims,
+                                          int32_t tokens, const void* K, const void* V, int64_t k_stride,
+                                          int64_t v_stride, const int32_t* pos, const int32_t* count,
+                                          sambay_stream_t stream);
+
+/*
+ * sambay_kv4_read - the values that positions pos[b] .. pos[b] + count[b] - 1
+ * stand for, as rows: K, V [B, tokens, Hkv, dh] io out, dense.  Rows from
+ * count[b] on are left as they were.
+ */
+SAMBAY_API sambay_status sambay_kv4_read(const sambay_kv4_cache* cache, const sambay_kv4_dims* dims,
+                                         int32_t tokens, void* K, void* V, const int32_t* pos,
+                                         const int32_t* count, sambay_stream_t stream);
+
+/*
+ * sambay_cross_attn_decode_kv4 - sambay_cross_attn_decode over the 4-bit cache:
+ * for the newest n = count[b] (NULL: tokens) tokens of each sequence, whose
+ * rows are the last n of the lens[b] cached ones,
+ *     out[b, t, h] = sum_j softmax_j(scale q[b, t, h] . K[b, j, h / G]) V[b, j, h / G]
+ * over j < lens[b] - (n - 1 - t): query t sees the cache up to its own token
+ * (with tokens = 1, all of it).  A query that sees no token gives 0; rows of
+ * out from n on are left as they were.
+ *
+ *   q, out [B, tokens, Hq, dh] io (out must not alias q); Hq a multiple of Hkv,
+ *   G = Hq / Hkv <= 16;  1 <= tokens <= 16;  lens [B] int32;  scale > 0, or 0
+ *   for 1 / sqrt(dh).
+ *   ws: >= sambay_cross_attn_decode_kv4_workspace(dims, q_heads, tokens); no
+ *   initialisation needed, not shared by two calls in flight at once.
+ * Products are float32 accumulations of f16 operands: what the cache holds is
+ * exact in f16, q is scaled per row by a power of two, and the probabilities
+ * are rounded to f16 (SAMBAY_F32: q and the probabilities are split into pairs
+ * of f16, 22 bits).
+ */
+SAMBAY_API size_t sambay_cross_attn_decode_kv4_workspace(const sambay_kv4_dims* dims, int32_t q_heads,
+                                                         int32_t tokens);
+SAMBAY_API sambay_status sambay_cross_attn_decode_kv4(const sambay_kv4_cache* cache, const sambay_kv4_dims* dims,
+                                                      int32_t q_heads, int32_t tokens, const void* q, void* out,
+                                                      const int32_t* lens, const int32_t* count, float scale,
+                                                      void* ws, size_t ws_bytes, sambay_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* SambaY-2: the memory readout of a Mamba-2 (SSD) layer                    */
