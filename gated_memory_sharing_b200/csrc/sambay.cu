@@ -1670,11 +1670,15 @@ sambay_status kv4_rows(bool write, const sambay_kv4_cache* c, const sambay_kv4_d
 
 constexpr int kKv4MaxTokens = 16;
 
-// Split-KV plan of the attention: enough (row tile, KV head, sequence, split)
-// CTAs to cover a 148-SM B200 about three times (a function of the sizes only).
+// The attention's grid, for a 148-SM B200 (a function of the sizes only, so
+// the workspace and the order of the sums do not depend on the device): the
+// resident CTAs, or fewer where the table has room for fewer tiles; and the
+// parts that each warp may leave of its first and its last pair.
 struct Kv4Plan {
-  int nt = 1, row_tiles = 1, splits = 1;
-  size_t o_part = 0, ml_part = 0, total = 0;
+  int nt = 1, row_tiles = 1, cols = 8, grid = 1;
+  bool one_tile = false;       // no pair has more than one tile: nothing is shared
+  bool many = false;           // about how many parts a pair has
+  size_t ml_part = 0, total = 0;
 };
 
 Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
@@ -1682,41 +1686,54 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   const int rows = q_heads / d->kv_heads * tokens;
   pl.nt = rows <= 8 ? 1 : 2;
   pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
-  const long long ctas = static_cast<long long>(d->batch) * d->kv_heads * pl.row_tiles;
-  constexpr int kBlock = sambay::kv4::kTile * sambay::kv4::kWarps;
-  const long long blocks = (static_cast<long long>(d->table_pages) * d->page_tokens + kBlock - 1) / kBlock;
-  pl.splits = static_cast<int>(std::min(blocks, std::max(1LL, (3LL * kSplitTarget + ctas - 1) / ctas)));
-  if (pl.splits > 1) {
-    const size_t cols = static_cast<size_t>(ctas) * pl.splits * 8 * pl.nt;
-    pl.ml_part = round256(cols * d->head_dim * 4);
-    pl.total = pl.ml_part + round256(cols * 2 * 4);
+  pl.cols = std::min(rows, 8 * pl.nt);
+  const long long pairs = static_cast<long long>(d->batch) * d->kv_heads * pl.row_tiles;
+  const long long tile = 4096 / d->head_dim;
+  const long long tiles = (static_cast<long long>(d->table_pages) * d->page_tokens + tile - 1) / tile;
+  const int ctas = sambay::kv4::attn_ctas(d->head_dim, pl.nt, d->io == SAMBAY_F32);
+  pl.grid = static_cast<int>(std::min(static_cast<long long>(kSplitTarget) * ctas, pairs * tiles));
+  pl.one_tile = tiles == 1;
+  pl.many = pl.grid * static_cast<long long>(sambay::kv4::kWarps) > 8 * pairs;
+  if (!pl.one_tile) {
+    const size_t parts = static_cast<size_t>(pl.grid) * sambay::kv4::kWarps * 2 * pl.cols;
+    pl.ml_part = round256(parts * d->head_dim * 4);
+    pl.total = pl.ml_part + round256(parts * 2 * 4);
   }
   return pl;
 }
 
 template <typename T, int D, int NT>
-sambay_status kv4_attn_launch(const sambay::kv4::AttnParams& p, cudaStream_t st) {
+sambay_status kv4_attn_launch(int dev, const sambay::kv4::AttnParams& p, const Kv4Plan& pl, cudaStream_t st) {
   using namespace sambay::kv4;
+  auto kern = kv4_attn_kernel<T, D, NT, sizeof(T) == 4>;
+  constexpr int kSmem = kWarps * kStages * kStageBytes;
+  static bool attr_set[kMaxDevices] = {};
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+      return SAMBAY_ERR_CUDA;
+    attr_set[dev] = true;
+  }
   {
     ProfScope ps("kv4_attn", st);
-    if (launch_k(kv4_attn_kernel<T, D, NT, sizeof(T) == 4>, dim3(p.splits * p.row_tiles, p.pg.Hkv, p.pg.B),
-                 dim3(kThreads), 0, st, false, 1, p) != cudaSuccess)
-      return SAMBAY_ERR_CUDA;
+    if (launch_k(kern, dim3(pl.grid), dim3(kThreads), kSmem, st, false, 1, p) != cudaSuccess) return SAMBAY_ERR_CUDA;
   }
-  if (p.splits > 1) {
-    const long long n = static_cast<long long>(p.pg.B) * p.T_ * p.Hq * D;
+  if (!pl.one_tile) {
+    const long long rows = static_cast<long long>(p.pg.B) * p.T_ * p.Hq;
     ProfScope ps("kv4_combine", st);
-    if (launch_k(kv4_combine_kernel<T, D, NT>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st, true,
-                 1, p) != cudaSuccess)
+    if (launch_k(pl.many ? kv4_combine_kernel<T, D, NT, 8> : kv4_combine_kernel<T, D, NT, 1>,
+                 dim3(static_cast<unsigned>(pl.many ? rows : (rows + 7) / 8)), dim3(256), 0, st, true, 1,
+                 p) != cudaSuccess)
       return SAMBAY_ERR_CUDA;
   }
   return SAMBAY_OK;
 }
 
 template <typename T>
-sambay_status kv4_attn(const sambay::kv4::AttnParams& p, int dh, int nt, cudaStream_t st) {
-  if (dh == 64) return nt == 1 ? kv4_attn_launch<T, 64, 1>(p, st) : kv4_attn_launch<T, 64, 2>(p, st);
-  return nt == 1 ? kv4_attn_launch<T, 128, 1>(p, st) : kv4_attn_launch<T, 128, 2>(p, st);
+sambay_status kv4_attn(int dev, const sambay::kv4::AttnParams& p, int dh, const Kv4Plan& pl, cudaStream_t st) {
+  if (dh == 64) return pl.nt == 1 ? kv4_attn_launch<T, 64, 1>(dev, p, pl, st) : kv4_attn_launch<T, 64, 2>(dev, p, pl, st);
+  return pl.nt == 1 ? kv4_attn_launch<T, 128, 1>(dev, p, pl, st) : kv4_attn_launch<T, 128, 2>(dev, p, pl, st);
 }
 
 sambay_status kv4_attn_check(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
@@ -1802,17 +1819,18 @@ sambay_status sambay_cross_attn_decode_kv4(const sambay_kv4_cache* c, const samb
   p.out = out;
   p.lens = lens;
   p.count = count;
-  p.o_part = pl.splits > 1 ? static_cast<float*>(ws) : nullptr;
-  p.ml_part = pl.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.ml_part) : nullptr;
+  p.o_part = pl.one_tile ? nullptr : static_cast<float*>(ws);
+  p.ml_part = pl.one_tile ? nullptr : reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.ml_part);
   p.T_ = tokens;
   p.Hq = q_heads;
   p.G = q_heads / d->kv_heads;
-  p.splits = pl.splits;
   p.row_tiles = pl.row_tiles;
+  p.cols = pl.cols;
+  p.warps = pl.grid * sambay::kv4::kWarps;
   const float sc = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d->head_dim));
   p.scale_log2 = sc * sambay::kLog2e;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return d->io == SAMBAY_BF16 ? kv4_attn<bf16>(p, d->head_dim, pl.nt, st) : kv4_attn<float>(p, d->head_dim, pl.nt, st);
+  return d->io == SAMBAY_BF16 ? kv4_attn<bf16>(dev, p, d->head_dim, pl, st) : kv4_attn<float>(dev, p, d->head_dim, pl, st);
 }
 
 // ------------------------------------------------------------ SambaY-2 (Mamba-2 SSD)

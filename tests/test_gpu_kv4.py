@@ -203,6 +203,8 @@ def filled(B, H, dh, page, lens, dtype, seed=20, **kw):
     (1, 9, 9, 64, 16, [333]),                # none share
     (1, 8, 1, 128, 16, [5000]),              # few sequences, many tokens
     (33, 10, 5, 64, 64, [(37 * i) % 200 for i in range(33)]),
+    (70, 4, 2, 128, 16, [(i * i * 31) % 1500 for i in range(70)]),
+    (40, 3, 3, 64, 16, [3000 if i == 7 else i % 3 for i in range(40)]),      # one long among short ones
 ])
 def test_attention(B, Hq, Hkv, dh, page, lens, dtype):
     c, K, V = filled(B, Hkv, dh, page, lens, dtype)
@@ -269,6 +271,30 @@ def test_what_is_not_the_sequences_is_not_read():
     # a NaN that belongs to the sequence is seen
     c.write(bad[:, :1].contiguous(), bad[:, :1].contiguous(), i32([3, 0]), i32([1, 0]))
     assert torch.isnan(c.attend(q, i32([n, 0]))[0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_nan_reaches_only_the_queries_that_see_it(dtype):
+    """Rows of NaN and infinity at newer tokens: older queries of the same call do not see them."""
+    for dh, n, T, at in ((64, 70, 4, 68), (128, 40, 6, 35), (64, 64, 3, 63), (128, 16, 2, 15)):
+        c, K, V = filled(1, 2, dh, 16, [n], dtype, seed=85)
+        q = rows(86, 1, T, 6, dh, dtype=dtype)
+        want = c.attend(q, i32([n]))
+        k, v = rows(85, 1, n, 2, dh, dtype=dtype)[:, at:at + 1].clone(), rows(86, 1, n, 2, dh, dtype=dtype)[:, at:at + 1].clone()
+        v[0, 0, 1, 20] = float("inf")              # one block of one head's V
+        c.write(k, v, i32([at]))
+        out = c.attend(q, i32([n]))
+        first = at - (n - T)                       # the first query that sees token `at`
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[0, first:, 3:, 16:32] = True
+        assert torch.equal(torch.isnan(out), hit)
+        assert torch.equal(out[:, :first], want[:, :first])
+        k[0, 0, 0, 3] = float("nan")               # and one of the other head's K
+        c.write(k, v, i32([at]))
+        hit[0, first:, :3] = True
+        out = c.attend(q, i32([n]))
+        assert torch.equal(torch.isnan(out), hit)
+        assert torch.equal(out[:, :first], want[:, :first])
 
 
 def test_pages_outside_the_pool_are_skipped_and_recorded():
