@@ -25,9 +25,10 @@
 //   K codes, 8 D bytes: per 64 values (blocks 4c .. 4c+3) 32 lanes x 16 bytes;
 //     lane (g, t): token g (8 bytes), token g + 8 (8 bytes), each 2 bytes per
 //     block b: values 16 b + 4 t .. + 3 (the lower nibble first)
-//   V codes, 8 D bytes: per 64 values 32 lanes x 16 bytes; lane (g, t): tokens
-//     2t, 2t + 1, 2t + 8, 2t + 9 (4 bytes each), one byte per block b: values
-//     16 b + 2 g, + 1
+//   V codes, 8 D bytes: per 64 values 32 lanes x 16 bytes; lane (g, t): four
+//     words of one byte per block b: value 16 b + 2 g of tokens 2t (lower
+//     nibble), 2t + 1; value 16 b + 2 g + 1 of these; and both of tokens 2t + 8,
+//     2t + 9
 //   K scales, D bytes: [g][token g, token g + 8][block]
 //   V scales, D bytes: [t][block][tokens 2t, 2t + 1, 2t + 8, 2t + 9]
 #pragma once
@@ -80,170 +81,9 @@ __device__ __forceinline__ uint8_t* group_of(const Pages& pg, int b, int h, int 
          (((static_cast<long long>(page) * pg.Hkv + h) << (pg.page_log2 - 4)) + in) * Block<D>::kBytes;
 }
 
-// ---------------------------------------------------------------- quantising
+// ---------------------------------------------------------------- rows in and out
 
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  const uint32_t m = code & 7u, e = code >> 3;                 // no sign
-  return e == 0 ? static_cast<float>(m) * 0.001953125f : __uint_as_float(((e + 120u) << 23) | (m << 20));
-}
-
-// e4m3 code of amax / 6, to nearest even, at most 448 (code 126).  The
-// conversion of the rounded quotient is off by one code at most; comparing
-// amax with 6 times the border on either side, exact in f32, settles it.
-__device__ __forceinline__ uint32_t block_scale(float amax) {
-  const float y = fminf(amax * 0.16666667f, 448.0f);
-  uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(y));
-  uint32_t c = two & 0x7Fu;
-  const float v = e4m3_value(c);
-  const float up = 3.0f * (v + e4m3_value(c + 1)), down = c > 0 ? 3.0f * (v + e4m3_value(c - 1)) : -1.0f;
-  if (c < 126 && (amax > up || (amax == up && (c & 1u)))) return c + 1;
-  if (amax < down || (amax == down && (c & 1u))) return c - 1;
-  return c;
-}
-
-// e2m1 code of x / s, to nearest even, saturating: the borders that |x|
-// passes, each exact in f32 (at most 7 bits).
-__device__ __forceinline__ uint32_t e2m1_code(float x, float s) {
-  const float a = fabsf(x);
-  uint32_t c = 0;
-  c += a > 0.25f * s;
-  c += a >= 0.75f * s;
-  c += a > 1.25f * s;
-  c += a >= 1.75f * s;
-  c += a > 2.5f * s;
-  c += a >= 3.5f * s;
-  c += a > 5.0f * s;
-  return s > 0.0f ? c | (x < 0.0f ? 8u : 0u) : 0u;             // also 0 where s is NaN
-}
-
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
-// The scale's code for a block whose largest |x| has the bits `m` (of a NaN or
-// an infinity if it holds one); *s receives the scale.
-__device__ __forceinline__ uint32_t scale_of(uint32_t m, float inv, float* s) {
-  if (m >= 0x7F800000u) {
-    *s = __int_as_float(0x7FC00000);
-    return 0x7Fu;
-  }
-  const uint32_t c = block_scale(__uint_as_float(m) * inv);
-  *s = e4m3_value(c);
-  return c;
-}
-
-template <typename T> __device__ __forceinline__ void load2(const T* p, float* x);
-template <> __device__ __forceinline__ void load2<float>(const float* p, float* x) {
-  const float2 v = *reinterpret_cast<const float2*>(p);
-  x[0] = v.x;
-  x[1] = v.y;
-}
-template <> __device__ __forceinline__ void load2<bf16>(const bf16* p, float* x) {
-  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-  x[0] = __uint_as_float(v << 16);
-  x[1] = __uint_as_float(v & 0xFFFF0000u);
-}
-__device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
-__device__ __forceinline__ void store2(bf16* p, float a, float b) {
-  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
-}
-
-template <typename T>
-struct RowParams {
-  Pages pg;
-  const T* K;              // write: rows, [B, T] tokens at k_stride elements
-  const T* V;
-  T* Ko;                   // read: rows [B, T, Hkv, D]
-  T* Vo;
-  const int32_t* pos;      // [B] cached tokens before the call's
-  const int32_t* count;    // [B] rows of each sequence, or null (T)
-  int T_;
-  long long k_stride, v_stride;
-};
-
-// Rows of sequence b: min(count, T) of them; a count outside 0 .. T is recorded.
-__device__ __forceinline__ int rows_of(const int32_t* count, int b, int T, bool tell) {
-  if (!count) return T;
-  const int n = count[b];
-  if ((n < 0 || n > T) && tell) record_status(kStatusBadIndex);
-  return max(0, min(T, n));
-}
-
-// One row of one head per 8 threads.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) kv4_write_kernel(const RowParams<T> p) {
-  const Pages& pg = p.pg;
-  const long long unit = (blockIdx.x * 256LL + threadIdx.x) >> 3;
-  const int j = threadIdx.x & 7;
-  const long long units = static_cast<long long>(pg.B) * p.T_ * pg.Hkv;
-  const bool in = unit < units;
-  const int h = in ? static_cast<int>(unit % pg.Hkv) : 0;
-  const long long row = in ? unit / pg.Hkv : 0;
-  const int b = static_cast<int>(row / p.T_), tok = static_cast<int>(row % p.T_);
-  const bool live = in && tok < rows_of(p.count, b, p.T_, h == 0 && tok == 0 && j == 0);
-  const int pos = static_cast<int>(static_cast<unsigned>(p.pos[b]) + tok);   // a wrapped sum is refused below
-  uint8_t* grp = live ? group_of<D>(pg, b, h, pos) : nullptr;
-  if (live && !grp && j == 0) record_status(kStatusBadIndex);
-  const int r = pos & 15, g = r & 7;
-  const T* kr = p.K + row * p.k_stride + h * D;
-  const T* vr = p.V + row * p.v_stride + h * D;
-  // every lane takes part in the shuffles; only lanes with a group load and store
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-    // K: thread (t = j % 4, half of the blocks): blocks 4c + 2 (j / 4), + 1
-    const float kinv = pow2i(-head_exp(pg.k_exp, h));
-    const int t = j & 3, b0 = 4 * c + 2 * (j >> 2);
-    uint32_t word = 0, sc = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (grp) {
-        load2(kr + 16 * (b0 + i) + 4 * t, x);
-        load2(kr + 16 * (b0 + i) + 4 * t + 2, x + 2);
-      }
-      uint32_t m = max(max(abs_bits(x[0]), abs_bits(x[1])), max(abs_bits(x[2]), abs_bits(x[3])));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      float s;
-      sc |= scale_of(m, kinv, &s) << (8 * i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) word |= e2m1_code(x[e] * kinv, s) << (16 * i + 4 * e);
-    }
-    if (grp) {
-      *reinterpret_cast<uint32_t*>(grp + Block<D>::kK + c * 512 + (g * 4 + t) * 16 + (r >> 3) * 8 + (j >> 2) * 4) = word;
-      if (t == 0)
-        *reinterpret_cast<uint16_t*>(grp + Block<D>::kKs + g * (D / 8) + (r >> 3) * (D / 16) + b0) =
-            static_cast<uint16_t>(sc);
-    }
-    // V: thread j holds values 16 b + 2 j, + 1 of blocks b = 4c .. 4c + 3
-    const float vinv = pow2i(-head_exp(pg.v_exp, h));
-    const int tv = g >> 1, w = (r & 1) + 2 * (r >> 3);
-    word = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x[2] = {0.f, 0.f};
-      if (grp) load2(vr + 16 * (4 * c + i) + 2 * j, x);
-      uint32_t m = max(abs_bits(x[0]), abs_bits(x[1]));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-      float s;
-      const uint32_t code = scale_of(m, vinv, &s);
-      word |= (e2m1_code(x[0] * vinv, s) | e2m1_code(x[1] * vinv, s) << 4) << (8 * i);
-      if (grp && j == i) grp[Block<D>::kVs + tv * (D / 4) + (4 * c + i) * 4 + w] = static_cast<uint8_t>(code);
-    }
-    if (grp) *reinterpret_cast<uint32_t*>(grp + Block<D>::kV + c * 512 + (j * 4 + tv) * 16 + w * 4) = word;
-  }
-}
-
-// ---------------------------------------------------------------- reading back
-
-// Two 4-bit values of a byte (the lower nibble in the lower half).
-__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t byte) {
-  uint32_t d;
-  asm("{\n\t.reg .b8 p;\n\tcvt.u8.u32 p, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, p;\n\t}" : "=r"(d) : "r"(byte));
-  return d;
-}
-// The four bytes of a word.
+// Two 4-bit values of each byte of a word, as f16 (the lower nibble in the lower half).
 __device__ __forceinline__ void e2m1x8_f16x2(uint32_t w, uint32_t (&d)[4]) {
   asm("{\n\t.reg .b8 p, q, r, s;\n\tmov.b32 {p, q, r, s}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, p;\n\tcvt.rn.f16x2.e2m1x2 %1, q;\n\t"
@@ -251,7 +91,7 @@ __device__ __forceinline__ void e2m1x8_f16x2(uint32_t w, uint32_t (&d)[4]) {
       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
       : "r"(w));
 }
-// Four e4m3 scales as f16 pairs (exact).
+// Four e4m3 scales as f16 pairs (exact; NaN stays NaN).
 __device__ __forceinline__ void e4m3x4_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, p;\n\tcvt.rn.f16x2.e4m3x2 %1, q;\n\t}"
       : "=r"(lo), "=r"(hi)
@@ -263,55 +103,364 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 __device__ __forceinline__ float2 f16x2_f32(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
-__device__ __forceinline__ float e4m3_or_nan(uint32_t code) {
-  return (code & 0x7Fu) == 0x7Fu ? __int_as_float(0x7FC00000) : e4m3_value(code & 0x7Fu);
+__device__ __forceinline__ uint32_t dup_lo(uint32_t v) { return __byte_perm(v, v, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t v) { return __byte_perm(v, v, 0x3232); }
+// 8 x 8 of 16 bits, rows over g and columns 2t, 2t + 1, transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t code) {          // without its sign; not of NaN
+  uint32_t two;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>(code)));
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(two)));
+}
+__device__ __forceinline__ uint32_t e4m3_code(float x) {              // nearest even, at most 448
+  uint16_t two;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(x));
+  return two & 0x7Fu;
+}
+// Bytes of two codes: e2m1(a) in the lower nibble, e2m1(b) in the upper one.
+__device__ __forceinline__ uint32_t e2m1_codes(float a, float b) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 p, z;\n\tmov.b16 {p, z}, 0;\n\tcvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
+      "mov.b32 %0, {p, z, z, z};\n\t}"
+      : "=r"(d)
+      : "f"(a), "f"(b));
+  return d;
 }
 
-// One row of one head per 8 threads, as kv4_write_kernel lays them out.
+// Four consecutive values of a row, and of them the largest |x|'s bits (those
+// of a NaN or an infinity are the largest), for each io type.
+//
+// Both roundings (amax / 6 to e4m3, x / s to e2m1) are made by the conversion
+// instructions from a product with a rounded reciprocal, at most 2^-21 off.
+// That decides rightly except where the exact quotient lies on a border
+// between two values (or, for f32, within the error of one).
+//   bf16: x and the border times the divisor have at most 8 significant bits,
+//     so a quotient that is not on a border is at least 2^-9 off it.  A factor
+//     of 1 + 2^-20 puts every quotient above its exact value, and cutting it to
+//     16 bits then gives a border exactly where it is one.
+//   f32: quotients within 2^-19 of a number of 4 bits (every border is one) are
+//     settled by comparing x with that number times the divisor, exact in f32.
+template <typename T> struct Four;
+template <> struct Four<bf16> {
+  uint2 v;
+  static constexpr uint32_t kInf = 0x7F80u;
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
+    return max(m & 0xFFFFu, m >> 16);
+  }
+  static __device__ __forceinline__ float top_value(uint32_t bits) { return __uint_as_float(bits << 16); }
+  static __device__ __forceinline__ float cut(float y) { return __uint_as_float(__float_as_uint(y) & 0xFFFFFF80u); }
+  // e4m3 code of amax / 6 * two; two: a power of two
+  static __device__ __forceinline__ uint32_t scale_code(float amax, float two) {
+    return e4m3_code(fminf(cut(amax * two * (0.16666667f * 1.00000095f)), 448.0f));
+  }
+  // the factor of e2m1's argument
+  static __device__ __forceinline__ float factor(float s, float two) { return __fdividef(1.00000095f, s) * two; }
+  __device__ __forceinline__ uint32_t codes(float fac, float, float) const {
+    const uint32_t lo = e2m1_codes(cut(__uint_as_float(v.x << 16) * fac), cut(__uint_as_float(v.x & 0xFFFF0000u) * fac));
+    const uint32_t hi = e2m1_codes(cut(__uint_as_float(v.y << 16) * fac), cut(__uint_as_float(v.y & 0xFFFF0000u) * fac));
+    return lo | hi << 8;
+  }
+};
+template <> struct Four<float> {
+  float4 v;
+  static constexpr uint32_t kInf = 0x7F800000u;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  static __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+  __device__ __forceinline__ uint32_t top() const {
+    return max(max(abs_bits(v.x), abs_bits(v.y)), max(abs_bits(v.z), abs_bits(v.w)));
+  }
+  static __device__ __forceinline__ float top_value(uint32_t bits) { return __uint_as_float(bits); }
+  static __device__ __forceinline__ uint32_t scale_code(float amax, float two) {
+    const float a = amax * two;
+    const uint32_t c = e4m3_code(fminf(a * 0.16666667f, 448.0f));
+    // off by one code at most: 6 times the border on either side
+    const float w = e4m3_value(c);
+    const float up = c < 126 ? 3.0f * (w + e4m3_value(c + 1)) : INFINITY;
+    const float down = c > 0 ? 3.0f * (w + e4m3_value(c - 1)) : -1.0f;
+    const bool odd = c & 1u;
+    if (a > up || (a == up && odd && c < 126)) return c + 1;
+    return a < down || (a == down && odd) ? c - 1 : c;
+  }
+  static __device__ __forceinline__ float factor(float s, float two) { return __fdividef(1.0f, s) * two; }
+  // x over s * 2^e, on the right side of a border that it is near (s2: s * 2^e)
+  static __device__ __forceinline__ float quotient(float x, float fac, float s, float two) {
+    const float y = x * fac;
+    const uint32_t yb = __float_as_uint(y);
+    if (((yb + 16u) & 0xFFFFFu) >= 32u) return y;
+    const uint32_t cb = (yb + 16u) & ~0xFFFFFu;
+    const float ax = fabsf(x * two), t = fabsf(__uint_as_float(cb)) * s;
+    return __uint_as_float(ax > t ? cb + 1u : ax < t && (cb & 0x7FFFFFFFu) ? cb - 1u : cb);
+  }
+  __device__ __forceinline__ uint32_t codes(float fac, float s, float two) const {
+    const uint32_t lo = e2m1_codes(quotient(v.x, fac, s, two), quotient(v.y, fac, s, two));
+    const uint32_t hi = e2m1_codes(quotient(v.z, fac, s, two), quotient(v.w, fac, s, two));
+    return lo | hi << 8;
+  }
+};
+
+__device__ __forceinline__ void store4(float* p, float2 a, float2 b) {
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(bf16* p, float2 a, float2 b) {
+  Pack16 u;
+  u.h2[0] = __floats2bfloat162_rn(a.x, a.y);
+  u.h2[1] = __floats2bfloat162_rn(b.x, b.y);
+  *reinterpret_cast<uint2*>(p) = make_uint2(u.u.x, u.u.y);
+}
+
+template <typename T>
+struct RowParams {
+  Pages pg;
+  const T* K;              // write: rows, [B, T] tokens at k_stride elements
+  const T* V;
+  T* Ko;                   // read: rows [B, T, Hkv, D]
+  T* Vo;
+  const int32_t* pos;      // [B] cached tokens before the call's
+  const int32_t* count;    // [B] rows of each sequence, or null (T)
+  int T_, groups;          // groups: of 16 tokens that T rows may touch, (T + 30) / 16
+  long long k_stride, v_stride;
+};
+
+// Rows of sequence b: min(count, T) of them; a count outside 0 .. T is recorded.
+__device__ __forceinline__ int rows_of(const int32_t* count, int b, int T, bool tell) {
+  if (!count) return T;
+  const int n = count[b];
+  if ((n < 0 || n > T) && tell) record_status(kStatusBadIndex);
+  return max(0, min(T, n));
+}
+
+// A warp's work in both directions: the 16 tokens of a group, 64 values of one
+// head.  Lane (g, t) has values 16 b + 4 t .. + 3 of blocks b = 0 .. 3 of
+// tokens g and g + 8 (half 0 and 1).
+template <int D>
+struct Unit {
+  int b, col;              // col: first value of the row's Hkv * D
+  int c;                   // 64-value part of the head
+  int row[2];              // the lane's two rows of the call, -1 where they are none
+  bool all;                // all 16 tokens are rows of the call
+  uint8_t* grp;            // null: nothing to do
+
+  template <typename T>
+  __device__ __forceinline__ Unit(const RowParams<T>& p, long long u) {
+    constexpr int C = D / 64;
+    const int heads = p.pg.Hkv * C;
+    const int hc = static_cast<int>(u % heads);
+    const long long k = u / heads;
+    b = static_cast<int>(k / p.groups);
+    col = hc * 64;
+    c = hc % C;
+    const int lane = threadIdx.x & 31;
+    const int n = rows_of(p.count, b, p.T_, hc == 0 && k % p.groups == 0);
+    const int pos = p.pos[b];
+    // the group's first position, and the call's rows in it
+    const long long at = ((static_cast<long long>(pos) >> 4) + k % p.groups) * kGroup;
+    grp = nullptr;
+    row[0] = row[1] = -1;
+    all = false;
+    if (n == 0 || at >= static_cast<long long>(pos) + n) return;
+    const int at32 = static_cast<int>(min(max(at, -1LL), 0x7FFFFFFFLL));      // what is cut is outside any table
+    grp = group_of<D>(p.pg, b, hc / C, at32);
+    if (!grp) {
+      if (lane == 0) record_status(kStatusBadIndex);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long r = at + (lane >> 2) + 8 * i - pos;
+      row[i] = r >= 0 && r < n ? static_cast<int>(r) : -1;
+    }
+    all = at >= pos && at + kGroup <= static_cast<long long>(pos) + n;
+  }
+};
+
+// What a warp keeps of one side (K or V): per half the codes (two words, 16
+// bits a block) and, in lane t = half (0 or 1), the word of the four scales.
+template <typename T>
+__device__ __forceinline__ void quantise(const Four<T> (&x)[2][4], float two, uint32_t (&codes)[2][2], uint32_t& scales) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
+  // the blocks' maxima over the four lanes; lane t ends with those of half t & 1, blocks 2 (t >> 1), + 1
+  uint32_t m[4], w[2];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t m0 = x[0][b].top(), m1 = x[1][b].top();
+    m[b] = max(t & 1 ? m1 : m0, __shfl_xor_sync(0xFFFFFFFFu, t & 1 ? m0 : m1, 1));
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+    w[b] = max(t & 2 ? m[2 + b] : m[b], __shfl_xor_sync(0xFFFFFFFFu, t & 2 ? m[b] : m[2 + b], 2));
+  uint32_t code = 0;
+  float s[2], fac[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const bool bad = w[b] >= Four<T>::kInf;
+    const uint32_t c = bad ? 0x7Fu : Four<T>::scale_code(Four<T>::top_value(w[b]), two);
+    s[b] = bad ? 0.0f : e4m3_value(c);
+    fac[b] = s[b] > 0.0f ? Four<T>::factor(s[b], two) : 0.0f;      // 0: codes of 0
+    code |= c << (8 * b);
+  }
+  scales = code | __shfl_xor_sync(0xFFFFFFFFu, code, 2) << 16;     // as it should be in lanes t = 0, 1
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t c16[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int src = (lane & ~3) | i | (b >> 1) << 1;
+      const float f = __shfl_sync(0xFFFFFFFFu, fac[b & 1], src);
+      const float sb = sizeof(T) == 4 ? __shfl_sync(0xFFFFFFFFu, s[b & 1], src) : 0.0f;
+      c16[b] = x[i][b].codes(f, sb, two);
+    }
+    codes[i][0] = c16[0] | c16[1] << 16;
+    codes[i][1] = c16[2] | c16[3] << 16;
+  }
+}
+
+// Codes of tokens g, g + 8 (K's order) to V's order and back: bytes of two
+// blocks move as 16 bits, 8 tokens by 8 pairs of values at a time.
+__device__ __forceinline__ void to_v_order(const uint32_t (&k)[2][2], uint32_t (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t r01 = movmatrix_trans(__byte_perm(k[i][0], 0, 0x3120));
+    const uint32_t r23 = movmatrix_trans(__byte_perm(k[i][1], 0, 0x3120));
+    const uint32_t w0 = __byte_perm(r01, r23, 0x5410), w1 = __byte_perm(r01, r23, 0x7632);   // tokens 2t, 2t + 1
+    v[2 * i] = (w0 & 0x0F0F0F0Fu) | (w1 << 4 & 0xF0F0F0F0u);
+    v[2 * i + 1] = (w0 >> 4 & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u);
+  }
+}
+__device__ __forceinline__ void from_v_order(const uint32_t (&v)[4], uint32_t (&k)[2][2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t e = v[2 * i], o = v[2 * i + 1];
+    const uint32_t w0 = (e & 0x0F0F0F0Fu) | (o << 4 & 0xF0F0F0F0u), w1 = (e >> 4 & 0x0F0F0F0Fu) | (o & 0xF0F0F0F0u);
+    k[i][0] = __byte_perm(movmatrix_trans(__byte_perm(w0, w1, 0x5410)), 0, 0x3120);
+    k[i][1] = __byte_perm(movmatrix_trans(__byte_perm(w0, w1, 0x7632)), 0, 0x3120);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void load_rows(const T* p, long long stride, const int (&row)[2], Four<T> (&x)[2][4]) {
+  const int t = threadIdx.x & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (row[i] >= 0)
+        x[i][b].load(p + row[i] * stride + 16 * b + 4 * t);
+      else
+        x[i][b].zero();
+}
+
+// Warp: one unit.  Bytes of the group that belong to other tokens keep their
+// values: K's codes and both scales are stored per token; of V's codes, where
+// two tokens share a byte, a group that is not all the call's is read first.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv4_write_kernel(const RowParams<T> p) {
+  const Pages& pg = p.pg;
+  const long long u = (blockIdx.x * 256LL + threadIdx.x) >> 5;
+  if (u >= static_cast<long long>(pg.B) * p.groups * pg.Hkv * (D / 64)) return;
+  const Unit<D> un(p, u);
+  if (!un.grp) return;                 // the whole warp's
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  constexpr int KS = D / 16;
+  Four<T> kx[2][4], vx[2][4];
+  load_rows(p.K + un.b * (p.T_ * p.k_stride) + un.col, p.k_stride, un.row, kx);
+  load_rows(p.V + un.b * (p.T_ * p.v_stride) + un.col, p.v_stride, un.row, vx);
+  uint32_t codes[2][2], scales;
+  quantise(kx, pow2i(-head_exp(pg.k_exp, un.col / D)), codes, scales);
+  {
+    uint8_t* dst = un.grp + Block<D>::kK + un.c * 512 + lane * 16;
+    if (un.all) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(codes[0][0], codes[0][1], codes[1][0], codes[1][1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (un.row[i] >= 0) *reinterpret_cast<uint2*>(dst + 8 * i) = make_uint2(codes[i][0], codes[i][1]);
+    }
+    if (t < 2 && (t ? un.row[1] : un.row[0]) >= 0)
+      *reinterpret_cast<uint32_t*>(un.grp + Block<D>::kKs + g * (2 * KS) + t * KS + 4 * un.c) = scales;
+  }
+  quantise(vx, pow2i(-head_exp(pg.v_exp, un.col / D)), codes, scales);
+  uint32_t v[4];
+  to_v_order(codes, v);
+  // scales: rows over tokens, columns (blocks 0 1, 2 3) of half 0 and of half 1
+  const uint32_t st = movmatrix_trans(t < 2 ? scales : 0u);
+  const uint32_t other = __shfl_down_sync(0xFFFFFFFFu, st, 8);              // half 1's
+  uint2 sv = make_uint2(__byte_perm(st, other, 0x6420), __byte_perm(st, other, 0x7531));
+  uint4* vdst = reinterpret_cast<uint4*>(un.grp + Block<D>::kV + un.c * 512 + lane * 16);
+  uint2* sdst = reinterpret_cast<uint2*>(un.grp + Block<D>::kVs + t * (4 * KS) + 16 * un.c + 8 * (g & 1));
+  if (!un.all) {
+    // whether tokens 2t, 2t + 1, 2t + 8, 2t + 9 are rows (bit 4 g of the ballots: token g's)
+    const uint32_t lo = __ballot_sync(0xFFFFFFFFu, un.row[0] >= 0), hi = __ballot_sync(0xFFFFFFFFu, un.row[1] >= 0);
+    const bool l0 = lo >> (8 * t) & 1, l1 = lo >> (8 * t + 4) & 1, h0 = hi >> (8 * t) & 1, h1 = hi >> (8 * t + 4) & 1;
+    const uint32_t ml = (l0 ? 0x0F0F0F0Fu : 0u) | (l1 ? 0xF0F0F0F0u : 0u), mh = (h0 ? 0x0F0F0F0Fu : 0u) | (h1 ? 0xF0F0F0F0u : 0u);
+    const uint4 old = *vdst;
+    v[0] = (v[0] & ml) | (old.x & ~ml);
+    v[1] = (v[1] & ml) | (old.y & ~ml);
+    v[2] = (v[2] & mh) | (old.z & ~mh);
+    v[3] = (v[3] & mh) | (old.w & ~mh);
+    if (g < 2) {
+      const uint32_t ms = (l0 ? 0xFFu : 0u) | (l1 ? 0xFF00u : 0u) | (h0 ? 0xFF0000u : 0u) | (h1 ? 0xFF000000u : 0u);
+      const uint2 was = *sdst;
+      sv.x = (sv.x & ms) | (was.x & ~ms);
+      sv.y = (sv.y & ms) | (was.y & ~ms);
+    }
+  }
+  *vdst = make_uint4(v[0], v[1], v[2], v[3]);
+  if (g < 2) *sdst = sv;
+}
+
+// The values of one side into its rows: codes and scales as quantise() gives them.
+template <typename T>
+__device__ __forceinline__ void store_rows(T* p, long long stride, const int (&row)[2], const uint32_t (&codes)[2][2],
+                                           uint32_t scales, float two) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t sl[2];
+    e4m3x4_f16x2(__shfl_sync(0xFFFFFFFFu, scales, (lane & ~3) | i), sl[0], sl[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t x[4];
+      e2m1x8_f16x2(codes[i][k], x);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t s = e ? dup_hi(sl[k]) : dup_lo(sl[k]);
+        float2 a = f16x2_f32(mul_f16x2(x[2 * e], s)), b = f16x2_f32(mul_f16x2(x[2 * e + 1], s));
+        a.x *= two; a.y *= two; b.x *= two; b.y *= two;
+        if (row[i] >= 0) store4(p + row[i] * stride + 16 * (2 * k + e) + 4 * t, a, b);
+      }
+    }
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const RowParams<T> p) {
   const Pages& pg = p.pg;
-  const long long unit = (blockIdx.x * 256LL + threadIdx.x) >> 3;
-  const int j = threadIdx.x & 7;
-  if (unit >= static_cast<long long>(pg.B) * p.T_ * pg.Hkv) return;
-  const int h = static_cast<int>(unit % pg.Hkv);
-  const long long row = unit / pg.Hkv;
-  const int b = static_cast<int>(row / p.T_), tok = static_cast<int>(row % p.T_);
-  if (tok >= rows_of(p.count, b, p.T_, h == 0 && tok == 0 && j == 0)) return;
-  const int pos = static_cast<int>(static_cast<unsigned>(p.pos[b]) + tok);   // a wrapped sum is refused below
-  const uint8_t* grp = group_of<D>(pg, b, h, pos);
-  if (!grp) {
-    if (j == 0) record_status(kStatusBadIndex);
-    return;
-  }
-  const int r = pos & 15, g = r & 7;
-  T* kr = p.Ko + unit * D;
-  T* vr = p.Vo + unit * D;
-  const float ke = pow2i(head_exp(pg.k_exp, h)), ve = pow2i(head_exp(pg.v_exp, h));
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-    const int t = j & 3, b0 = 4 * c + 2 * (j >> 2);
-    uint32_t v[4];
-    e2m1x8_f16x2(*reinterpret_cast<const uint32_t*>(grp + Block<D>::kK + c * 512 + (g * 4 + t) * 16 + (r >> 3) * 8 +
-                                                    (j >> 2) * 4), v);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float s = e4m3_or_nan(grp[Block<D>::kKs + g * (D / 8) + (r >> 3) * (D / 16) + b0 + i]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 x = f16x2_f32(v[2 * i + e]);
-        store2(kr + 16 * (b0 + i) + 4 * t + 2 * e, x.x * s * ke, x.y * s * ke);
-      }
-    }
-    const int tv = g >> 1, w = (r & 1) + 2 * (r >> 3);
-    e2m1x8_f16x2(*reinterpret_cast<const uint32_t*>(grp + Block<D>::kV + c * 512 + (j * 4 + tv) * 16 + w * 4), v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float s = e4m3_or_nan(grp[Block<D>::kVs + tv * (D / 4) + (4 * c + i) * 4 + w]);
-      const float2 x = f16x2_f32(v[i]);
-      store2(vr + 16 * (4 * c + i) + 2 * j, x.x * s * ve, x.y * s * ve);
-    }
-  }
+  const long long u = (blockIdx.x * 256LL + threadIdx.x) >> 5;
+  if (u >= static_cast<long long>(pg.B) * p.groups * pg.Hkv * (D / 64)) return;
+  const Unit<D> un(p, u);
+  if (!un.grp) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  constexpr int KS = D / 16;
+  const uint4 kc = *reinterpret_cast<const uint4*>(un.grp + Block<D>::kK + un.c * 512 + lane * 16);
+  const uint4 vc = *reinterpret_cast<const uint4*>(un.grp + Block<D>::kV + un.c * 512 + lane * 16);
+  const uint32_t ks = *reinterpret_cast<const uint32_t*>(un.grp + Block<D>::kKs + g * (2 * KS) + (t & 1) * KS + 4 * un.c);
+  const uint2 sv = *reinterpret_cast<const uint2*>(un.grp + Block<D>::kVs + t * (4 * KS) + 16 * un.c + 8 * (g & 1));
+  const long long stride = static_cast<long long>(pg.Hkv) * D, base = un.b * (p.T_ * stride) + un.col;
+  uint32_t codes[2][2] = {{kc.x, kc.y}, {kc.z, kc.w}};
+  store_rows(p.Ko + base, stride, un.row, codes, ks, pow2i(head_exp(pg.k_exp, un.col / D)));
+  const uint32_t v[4] = {vc.x, vc.y, vc.z, vc.w};
+  from_v_order(v, codes);
+  // rows (blocks 0 1, 2 3) of half 0, of half 1; columns over tokens
+  const uint32_t vs = movmatrix_trans(g & 2 ? __byte_perm(sv.x, sv.y, 0x7362) : __byte_perm(sv.x, sv.y, 0x5140));
+  store_rows(p.Vo + base, stride, un.row, codes, vs, pow2i(head_exp(pg.v_exp, un.col / D)));
 }
 
 // ---------------------------------------------------------------- attention
@@ -362,17 +511,25 @@ __device__ __forceinline__ void mma16816_f16(float (&d)[4], uint32_t a0, uint32_
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
-  uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t dup_lo(uint32_t v) { return __byte_perm(v, v, 0x1010); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t v) { return __byte_perm(v, v, 0x3232); }
+template <typename T> __device__ __forceinline__ void load2(const T* p, float* x);
+template <> __device__ __forceinline__ void load2<float>(const float* p, float* x) {
+  const float2 v = *reinterpret_cast<const float2*>(p);
+  x[0] = v.x;
+  x[1] = v.y;
+}
+template <> __device__ __forceinline__ void load2<bf16>(const bf16* p, float* x) {
+  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+  x[0] = __uint_as_float(v << 16);
+  x[1] = __uint_as_float(v & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store2(bf16* p, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -692,10 +849,10 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
         const uint4 sv = *reinterpret_cast<const uint4*>(grp + Block<D>::kVs + t * (D / 4) + k * 16);
         uint32_t scw[4] = {sv.x & keep, sv.y & keep, sv.z & keep, sv.w & keep};
         uint32_t x0[4], x1[4], x2[4], x3[4];
-        e2m1x8_f16x2((v.x & 0x0F0F0F0Fu) | ((v.y << 4) & 0xF0F0F0F0u), x0);     // values 2g, tokens 2t, 2t + 1
-        e2m1x8_f16x2(((v.x >> 4) & 0x0F0F0F0Fu) | (v.y & 0xF0F0F0F0u), x1);     // values 2g + 1
-        e2m1x8_f16x2((v.z & 0x0F0F0F0Fu) | ((v.w << 4) & 0xF0F0F0F0u), x2);     // values 2g, tokens 2t + 8, 2t + 9
-        e2m1x8_f16x2(((v.z >> 4) & 0x0F0F0F0Fu) | (v.w & 0xF0F0F0F0u), x3);
+        e2m1x8_f16x2(v.x, x0);         // values 2g, tokens 2t, 2t + 1
+        e2m1x8_f16x2(v.y, x1);         // values 2g + 1
+        e2m1x8_f16x2(v.z, x2);         // values 2g, tokens 2t + 8, 2t + 9
+        e2m1x8_f16x2(v.w, x3);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           int bad = 0x7FFFFFFF;                       // first token of the group whose block is NaN

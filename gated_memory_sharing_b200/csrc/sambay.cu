@@ -1632,20 +1632,20 @@ sambay::kv4::Pages kv4_pages(const sambay_kv4_cache* c, const sambay_kv4_dims* d
   return pg;
 }
 
-// Rows of a write or read: B * tokens * Hkv of them, 32 a CTA.
+// Rows of a write or read.
 sambay_status kv4_check_rows(const sambay_kv4_dims* d, int32_t tokens) {
   if (tokens < 1) return SAMBAY_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(d->batch) * tokens;
-  if (rows > (1LL << 36) / d->kv_heads) return SAMBAY_ERR_UNSUPPORTED;
+  if (rows > (1LL << 33) / d->kv_heads) return SAMBAY_ERR_UNSUPPORTED;   // CTAs within a grid's 2^31
   return SAMBAY_OK;
 }
 
 template <typename T, int D>
 sambay_status kv4_rows_launch(bool write, const sambay::kv4::RowParams<T>& p, cudaStream_t st) {
-  const long long units = static_cast<long long>(p.pg.B) * p.T_ * p.pg.Hkv;
+  const long long units = static_cast<long long>(p.pg.B) * p.groups * p.pg.Hkv * (D / 64);
   auto kern = write ? sambay::kv4::kv4_write_kernel<T, D> : sambay::kv4::kv4_read_kernel<T, D>;
   ProfScope ps(write ? "kv4_write" : "kv4_read", st);
-  return launch_k(kern, dim3(static_cast<unsigned>((units + 31) / 32)), dim3(256), 0, st, false, 1, p) == cudaSuccess
+  return launch_k(kern, dim3(static_cast<unsigned>((units + 7) / 8)), dim3(256), 0, st, false, 1, p) == cudaSuccess
              ? SAMBAY_OK
              : SAMBAY_ERR_CUDA;
 }
@@ -1663,6 +1663,7 @@ sambay_status kv4_rows(bool write, const sambay_kv4_cache* c, const sambay_kv4_d
   p.pos = pos;
   p.count = count;
   p.T_ = tokens;
+  p.groups = static_cast<int>((tokens + 30LL) / 16);
   p.k_stride = k_stride;
   p.v_stride = v_stride;
   return d->head_dim == 64 ? kv4_rows_launch<T, 64>(write, p, st) : kv4_rows_launch<T, 128>(write, p, st);
