@@ -335,8 +335,21 @@ def sambay_cross_attn_decode(dims: AttnDims, q, K, V, out, scale: float, ws, str
         ctypes.byref(dims), _p(q), _p(K), _p(V), _p(out), scale, _p(ws), ws_bytes, _stream(stream)))
 
 
+# The 4-bit cache's calls run once per layer and decoded token, where the
+# host's microseconds show: they pass plain addresses and take the stream as a
+# handle too.
+
+def _a(t):
+    """Address of a tensor (None -> NULL)."""
+    return None if t is None else t.data_ptr()
+
+
+def _handle(stream):
+    return stream if type(stream) is int else _stream(stream)
+
+
 def make_kv4_cache(pages, table, k_exp=None, v_exp=None) -> Kv4Cache:
-    return Kv4Cache(*(None if t is None else t.data_ptr() for t in (pages, table, k_exp, v_exp)))
+    return Kv4Cache(_a(pages), _a(table), _a(k_exp), _a(v_exp))
 
 
 def sambay_kv4_cache_bytes(dims: Kv4Dims) -> int:
@@ -345,14 +358,17 @@ def sambay_kv4_cache_bytes(dims: Kv4Dims) -> int:
 
 def sambay_kv4_write(cache: Kv4Cache, dims: Kv4Dims, tokens: int, K, V, pos, count=None, k_stride: int = 0,
                      v_stride: int = 0, stream=None):
-    _check("sambay_kv4_write", load().sambay_kv4_write(
-        ctypes.byref(cache), ctypes.byref(dims), tokens, _p(K), _p(V), k_stride, v_stride, _p(pos), _p(count),
-        _stream(stream)))
+    code = load().sambay_kv4_write(ctypes.byref(cache), ctypes.byref(dims), tokens, _a(K), _a(V), k_stride, v_stride,
+                                   _a(pos), _a(count), _handle(stream))
+    if code:
+        raise SambayError("sambay_kv4_write", code)
 
 
 def sambay_kv4_read(cache: Kv4Cache, dims: Kv4Dims, tokens: int, K, V, pos, count=None, stream=None):
-    _check("sambay_kv4_read", load().sambay_kv4_read(
-        ctypes.byref(cache), ctypes.byref(dims), tokens, _p(K), _p(V), _p(pos), _p(count), _stream(stream)))
+    code = load().sambay_kv4_read(ctypes.byref(cache), ctypes.byref(dims), tokens, _a(K), _a(V), _a(pos), _a(count),
+                                  _handle(stream))
+    if code:
+        raise SambayError("sambay_kv4_read", code)
 
 
 def sambay_cross_attn_decode_kv4_workspace(dims: Kv4Dims, q_heads: int, tokens: int) -> int:
@@ -360,11 +376,13 @@ def sambay_cross_attn_decode_kv4_workspace(dims: Kv4Dims, q_heads: int, tokens: 
 
 
 def sambay_cross_attn_decode_kv4(cache: Kv4Cache, dims: Kv4Dims, q_heads: int, tokens: int, q, out, lens, count,
-                                 scale: float, ws, stream=None):
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check("sambay_cross_attn_decode_kv4", load().sambay_cross_attn_decode_kv4(
-        ctypes.byref(cache), ctypes.byref(dims), q_heads, tokens, _p(q), _p(out), _p(lens), _p(count), scale, _p(ws),
-        ws_bytes, _stream(stream)))
+                                 scale: float, ws, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    code = load().sambay_cross_attn_decode_kv4(ctypes.byref(cache), ctypes.byref(dims), q_heads, tokens, _a(q), _a(out),
+                                               _a(lens), _a(count), scale, _a(ws), ws_bytes, _handle(stream))
+    if code:
+        raise SambayError("sambay_cross_attn_decode_kv4", code)
 
 
 def sambay_ssd_prefill_workspace(dims: SsdDims) -> int:

@@ -476,6 +476,8 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 4608;
+constexpr int kSmemBytes = kWarps * (kStages * kStageBytes + kStages * 8);
+constexpr long long kWaitCycles = 1LL << 31;     // a copy that has not come after about a second
 // Probabilities are kept times 2^15 (the largest of a row is 2^15): as f16 they
 // then have 11 bits down to 2^-29 of the largest instead of 2^-14, which shows
 // where the likeliest tokens' values are zero.  Numerator and denominator carry
@@ -530,12 +532,69 @@ __device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpre
 __device__ __forceinline__ void store2(bf16* p, float a, float b) {
   *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// The same with a zero accumulator in.
+__device__ __forceinline__ void mma16816_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                  uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Pairs of f32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// A warp's ring: bulk copies that complete on one mbarrier a stage.
+__device__ __forceinline__ void bar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  if (bar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!bar_try(bar, parity))
+    if (clock64() - t0 > kWaitCycles) return false;
+  return true;
+}
+// Untiled copy of whole 16 bytes to this CTA's shared memory (no multicast).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 
 // Cached tokens of sequence b, inside the table; `tell` records a length outside it.
 __device__ __forceinline__ int len_of(const AttnParams& p, int b, bool tell) {
@@ -639,7 +698,6 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   constexpr int KS = D / 16;
   constexpr int NQ = SPLIT ? 2 : 1;
   constexpr int TILE = 4096 / D, GP = TILE / kGroup;
-  constexpr int kChunks = Block<D>::kBytes / 16;      // 16-byte pieces of a group
   extern __shared__ __align__(128) uint8_t smem[];
   const Pages& pg = p.pg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -648,12 +706,16 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   const int gw = warp * gridDim.x + blockIdx.x;
   uint8_t* ring = smem + warp * (kStages * kStageBytes);
   const uint32_t ring_addr = shared_addr(ring);
+  const uint32_t bars = shared_addr(smem + kWarps * kStages * kStageBytes) + warp * (kStages * 8);
 
   long long none;
   const Line line = line_of<D>(p, 0, gw == 0, &none);
   if (gw >= line.shares) return;
   const long long begin = line.begin(gw);
   const int share = static_cast<int>(line.begin(gw + 1) - begin);
+  if (lane < kStages) bar_init(bars + 8 * lane);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();
 
   Cursor in = find<D>(p, begin);       // the next tile to load
   Cursor c = in;                       // the tile being worked on
@@ -661,58 +723,52 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   // Pages of the 32 groups of the loading cursor's window (512 tokens), one a lane.
   int win_b = -1, win = -1, page = -1;
   uint32_t have = 0;                   // GP bits a stage: which groups were loaded
-  auto issue = [&](int i, int st) {
-    if (i < share) {
-      const int tok0 = in.tile * TILE;
-      if (in.b != win_b || (tok0 >> 9) != win) {
-        win_b = in.b;
-        win = tok0 >> 9;
-        const int tok = win * 512 + lane * kGroup;
-        page = -1;
-        if (tok < in.len) {
-          page = pg.table[static_cast<long long>(in.b) * pg.table_pages + (tok >> pg.page_log2)];
-          if (page < 0 || page >= pg.num_pages) {
-            page = -1;
-            record_status(kStatusBadIndex);
-          }
+  auto issue = [&](int st) {
+    const int tok0 = in.tile * TILE;
+    if (in.b != win_b || (tok0 >> 9) != win) {
+      win_b = in.b;
+      win = tok0 >> 9;
+      const int tok = win * 512 + lane * kGroup;
+      page = -1;
+      if (tok < in.len) {
+        page = pg.table[static_cast<long long>(in.b) * pg.table_pages + (tok >> pg.page_log2)];
+        if (page < 0 || page >= pg.num_pages) {
+          page = -1;
+          record_status(kStatusBadIndex);
         }
       }
-      const int h = in.pair / p.row_tiles;
-      uint32_t mask = 0;
-#pragma unroll
-      for (int q = 0; q < GP; ++q) {
-        const int tok = tok0 + q * kGroup;
-        const int pid = __shfl_sync(0xFFFFFFFFu, page, (tok >> 4) & 31);
-        if (pid >= 0) {
-          mask |= 1u << q;
-          const int at = (tok & ((1 << pg.page_log2) - 1)) / kGroup;
-          const uint8_t* src =
-              pg.cache + (((static_cast<long long>(pid) * pg.Hkv + h) << (pg.page_log2 - 4)) + at) * Block<D>::kBytes;
-          const uint32_t dst = ring_addr + st * kStageBytes + q * Block<D>::kBytes;
-#pragma unroll
-          for (int k = 0; k < (kChunks + 31) / 32; ++k) {
-            const int x = lane + 32 * k;
-            if (x < kChunks) cp_async16(dst + x * 16, src + x * 16);
-          }
-        }
-      }
-      have = (have & ~(((1u << GP) - 1) << (GP * st))) | mask << (GP * st);
-      advance<D>(p, in);
     }
-    cp_async_commit();
+    // lane q: group q of the tile
+    const int pid = __shfl_sync(0xFFFFFFFFu, page, (tok0 >> 4) + lane);
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lane < GP && pid >= 0);
+    const int h = in.pair / p.row_tiles;
+    const int at = ((tok0 + lane * kGroup) & ((1 << pg.page_log2) - 1)) / kGroup;
+    const uint8_t* src =
+        pg.cache + (((static_cast<long long>(pid) * pg.Hkv + h) << (pg.page_log2 - 4)) + at) * Block<D>::kBytes;
+    const uint32_t dst = ring_addr + st * kStageBytes, bar = bars + 8 * st;
+    if (lane == 0) bar_expect(bar, __popc(mask) * Block<D>::kBytes);
+    if ((1 << pg.page_log2) >= TILE) {               // one piece: the groups below the sequence's end
+      if (lane == 0 && mask) bulk_load(dst, src, __popc(mask) * Block<D>::kBytes, bar);
+    } else if (mask >> lane & 1) {
+      bulk_load(dst + lane * Block<D>::kBytes, src, Block<D>::kBytes, bar);
+    }
+    have = (have & ~(((1u << GP) - 1) << (GP * st))) | mask << (GP * st);
+    advance<D>(p, in);
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+  for (int i = 0; i < kStages - 1; ++i)
+    if (i < share) issue(i);
 
   uint32_t qb[NQ][NT][KS][2];
   float f[NT][2];
   int lim[NT][2];
-  float m[NT][2], l[NT][2], o[NT][KS][4];
+  float m[NT][2], ref[NT][2], l[NT][2], o[NT][KS][4];      // ref: what exponents are relative to
   bool fresh = true;
   int st = 0, lim_min = 0;
+  uint32_t parity = 0;
 
   for (int i = 0; i < share; ++i) {
-    issue(i + kStages - 1, st == 0 ? kStages - 1 : st - 1);
+    if (i + kStages - 1 < share) issue(st == 0 ? kStages - 1 : st - 1);
     if (fresh) {
       // B fragments of Q (column g of n-tile n), and per accumulator column its factor and its last token
       fresh = false;
@@ -768,6 +824,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
           f[n][e] = __shfl_sync(0xFFFFFFFFu, fac, (2 * t + e) * 4);
           lim[n][e] = min(c.len, __shfl_sync(0xFFFFFFFFu, limit, (2 * t + e) * 4));
           m[n][e] = -INFINITY;
+          ref[n][e] = 0.0f;
           l[n][e] = 0.0f;
         }
 #pragma unroll
@@ -775,8 +832,15 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
       }
       lim_min = __reduce_min_sync(0xFFFFFFFFu, lim_min);
     }
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
+    if (!bar_wait(bars + 8 * st, parity)) {
+      // lost: tell, and leave when the copies in flight have come (or again do not)
+      record_status(kStatusTimeout);
+      for (int k = i; k < min(share, i + kStages); ++k) {
+        bar_wait(bars + 8 * st, parity);
+        if (++st == kStages) st = 0, parity ^= 1;
+      }
+      return;
+    }
 
     const int tok0 = c.tile * TILE;
     const uint32_t mask = have >> (GP * st) & ((1u << GP) - 1);
@@ -808,17 +872,35 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
           uint32_t x0[4], x1[4];                     // tokens g and g + 8
           e2m1x8_f16x2(kc[4 * k + bp], x0);
           e2m1x8_f16x2(kc[4 * k + 2 + bp], x1);
+          const float2 f0 = f16x2_f32(sl[0][bp]), f1 = f16x2_f32(sl[1][bp]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t s0 = e ? dup_hi(sl[0][bp]) : dup_lo(sl[0][bp]);
-            const uint32_t s1 = e ? dup_hi(sl[1][bp]) : dup_lo(sl[1][bp]);
-            const uint32_t a0 = mul_f16x2(x0[2 * e], s0), a1 = mul_f16x2(x1[2 * e], s1);
-            const uint32_t a2 = mul_f16x2(x0[2 * e + 1], s0), a3 = mul_f16x2(x1[2 * e + 1], s1);
             const int kb = 4 * k + 2 * bp + e;
+            if (NT == 1) {
+              // the block's scales on its products: 4 operations, as many as on
+              // the codes, but none on the pipe that converts them
+              float d[4];
+              mma16816_f16_zero(d, x0[2 * e], x1[2 * e], x0[2 * e + 1], x1[2 * e + 1], qb[0][0][kb][0], qb[0][0][kb][1]);
+              if (SPLIT)
+                mma16816_f16(d, x0[2 * e], x1[2 * e], x0[2 * e + 1], x1[2 * e + 1], qb[NQ - 1][0][kb][0], qb[NQ - 1][0][kb][1]);
+              const float s0 = e ? f0.y : f0.x, s1 = e ? f1.y : f1.x;
+              s[0][q][0] = kb == 0 ? d[0] * s0 : fmaf(d[0], s0, s[0][q][0]);
+              s[0][q][1] = kb == 0 ? d[1] * s0 : fmaf(d[1], s0, s[0][q][1]);
+              s[0][q][2] = kb == 0 ? d[2] * s1 : fmaf(d[2], s1, s[0][q][2]);
+              s[0][q][3] = kb == 0 ? d[3] * s1 : fmaf(d[3], s1, s[0][q][3]);
+            } else {
+              const uint32_t s0 = e ? dup_hi(sl[0][bp]) : dup_lo(sl[0][bp]);
+              const uint32_t s1 = e ? dup_hi(sl[1][bp]) : dup_lo(sl[1][bp]);
+              const uint32_t a0 = mul_f16x2(x0[2 * e], s0), a1 = mul_f16x2(x1[2 * e], s1);
+              const uint32_t a2 = mul_f16x2(x0[2 * e + 1], s0), a3 = mul_f16x2(x1[2 * e + 1], s1);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816_f16(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
-              if (SPLIT) mma16816_f16(s[n][q], a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
+              for (int n = 0; n < NT; ++n) {
+                if (kb == 0)
+                  mma16816_f16_zero(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
+                else
+                  mma16816_f16(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
+                if (SPLIT) mma16816_f16(s[n][q], a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
+              }
             }
           }
         }
@@ -882,10 +964,6 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
         }
       }
     };
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < GP; ++q) s[n][q][0] = s[n][q][1] = s[n][q][2] = s[n][q][3] = 0.0f;
     const bool whole = mask == (1u << GP) - 1 && tok0 + TILE <= lim_min;   // every column sees every token
     if (whole) {
 #pragma unroll
@@ -902,33 +980,57 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
       }
     }
     // online softmax per column: the factor f > 0, so the largest s is the largest logit
+    float mx[NT][2];
+    bool grown = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = -INFINITY;
+        mx[n][e] = fmaxf(s[n][0][e], s[n][0][e + 2]);
 #pragma unroll
-        for (int q = 0; q < GP; ++q) mx = fmaxf(mx, fmaxf(s[n][q][e], s[n][q][e + 2]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-        const float mn = fmaxf(m[n][e], mx * f[n][e]);
-        const float ref = mn == -INFINITY ? 0.0f : mn - kPShift;        // a column that sees none of these tokens
-        const float corr = mn == -INFINITY ? 0.0f : ex2_approx(m[n][e] - mn);
-        m[n][e] = mn;
-        l[n][e] *= corr;
+        for (int q = 1; q < GP; ++q) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[n][q][e], s[n][q][e + 2]));
+        mx[n][e] *= f[n][e];
+        grown |= mx[n][e] > m[n][e];
+      }
+    if (__any_sync(0xFFFFFFFFu, grown)) {      // most tiles hold no new maximum
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float corr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = mx[n][e];
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+          const float mn = fmaxf(m[n][e], x);
+          corr[e] = mn == -INFINITY ? 0.0f : ex2_approx(m[n][e] - mn);
+          m[n][e] = mn;
+          ref[n][e] = mn == -INFINITY ? 0.0f : kPShift - mn;        // a column that sees none of these tokens
+          l[n][e] *= corr[e];
+        }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          o[n][k][e] *= corr;
-          o[n][k][e + 2] *= corr;
-        }
-#pragma unroll
-        for (int q = 0; q < GP; ++q) {
-          s[n][q][e] = ex2_approx(fmaf(s[n][q][e], f[n][e], -ref));
-          s[n][q][e + 2] = ex2_approx(fmaf(s[n][q][e + 2], f[n][e], -ref));
-          l[n][e] += s[n][q][e] + s[n][q][e + 2];
+          const float2 u = mul2(make_float2(o[n][k][0], o[n][k][1]), make_float2(corr[0], corr[1]));
+          const float2 v = mul2(make_float2(o[n][k][2], o[n][k][3]), make_float2(corr[0], corr[1]));
+          o[n][k][0] = u.x; o[n][k][1] = u.y; o[n][k][2] = v.x; o[n][k][3] = v.y;
         }
       }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float2 fn = make_float2(f[n][0], f[n][1]), rn = make_float2(ref[n][0], ref[n][1]);
+      float2 ln = make_float2(l[n][0], l[n][1]);
+#pragma unroll
+      for (int q = 0; q < GP; ++q) {
+        const float2 u = fma2(make_float2(s[n][q][0], s[n][q][1]), fn, rn);
+        const float2 v = fma2(make_float2(s[n][q][2], s[n][q][3]), fn, rn);
+        s[n][q][0] = ex2_approx(u.x); s[n][q][1] = ex2_approx(u.y);
+        s[n][q][2] = ex2_approx(v.x); s[n][q][3] = ex2_approx(v.y);
+        ln = add2(ln, add2(make_float2(s[n][q][0], s[n][q][1]), make_float2(s[n][q][2], s[n][q][3])));
+      }
+      l[n][0] = ln.x;
+      l[n][1] = ln.y;
+    }
     if (whole) {
 #pragma unroll
       for (int q = 0; q < GP; ++q) outputs(q, 0xFFFFFFFFu, std::false_type());
@@ -944,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
       }
     }
     __syncwarp();                      // the stage is read; the next iteration's copies may refill it
-    st = st == kStages - 1 ? 0 : st + 1;
+    if (++st == kStages) st = 0, parity ^= 1;
 
     if (c.tile + 1 == c.tiles || i + 1 == share) {
       // the pair, or this warp's share of it, is done

@@ -1707,10 +1707,9 @@ template <typename T, int D, int NT>
 sambay_status kv4_attn_launch(int dev, const sambay::kv4::AttnParams& p, const Kv4Plan& pl, cudaStream_t st) {
   using namespace sambay::kv4;
   auto kern = kv4_attn_kernel<T, D, NT, sizeof(T) == 4>;
-  constexpr int kSmem = kWarps * kStages * kStageBytes;
   static bool attr_set[kMaxDevices] = {};
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
         cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess)
       return SAMBAY_ERR_CUDA;
@@ -1718,7 +1717,7 @@ sambay_status kv4_attn_launch(int dev, const sambay::kv4::AttnParams& p, const K
   }
   {
     ProfScope ps("kv4_attn", st);
-    if (launch_k(kern, dim3(pl.grid), dim3(kThreads), kSmem, st, false, 1, p) != cudaSuccess) return SAMBAY_ERR_CUDA;
+    if (launch_k(kern, dim3(pl.grid), dim3(kThreads), kSmemBytes, st, false, 1, p) != cudaSuccess) return SAMBAY_ERR_CUDA;
   }
   if (!pl.one_tile) {
     const long long rows = static_cast<long long>(p.pg.B) * p.T_ * p.Hq;

@@ -311,7 +311,9 @@ class KV4Cache:
     def __init__(self, batch: int, kv_heads: int, head_dim: int, max_tokens: int, page_tokens: int = 64,
                  io: int = abi.BF16, num_pages=None, table=None, k_exp=None, v_exp=None, device="cuda"):
         self.device = torch.device(device)
-        if self.device.type == "cuda" and self.device.index is None:
+        if self.device.type != "cuda":
+            raise ValueError(f"the cache lies on a GPU, not on {self.device}")
+        if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         each = -(-max_tokens // page_tokens)
         if table is None:
@@ -322,6 +324,7 @@ class KV4Cache:
             table = torch.arange(batch * each, dtype=torch.int32, device=self.device).view(batch, each)
         elif num_pages is None:
             raise ValueError("a table needs num_pages, the pool's size")
+        self._dev = self.device.index
         self.io, self.dtype = io, io_dtype(io)
         self.batch, self.kv_heads, self.head_dim, self.page_tokens = batch, kv_heads, head_dim, page_tokens
         self.table, self.k_exp, self.v_exp = table, k_exp, v_exp
@@ -340,7 +343,7 @@ class KV4Cache:
             # zeros: a page that was never written reads as zeros
             self.pages = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.abi_cache = abi.make_kv4_cache(self.pages, table, k_exp, v_exp)
-        self._ws_bytes = {}
+        self._plans = {}
 
     @staticmethod
     def exponents(rows) -> torch.Tensor:
@@ -353,19 +356,22 @@ class KV4Cache:
     # ------------------------------------------------------------- checks
 
     def _index(self, t, name, n):
-        if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or (n is not None and t.numel() != n):
-            raise ValueError(f"{name}: {'an' if n is None else n} int32 dense on {self.device}, "
+        if t.dtype is not torch.int32 or t.get_device() != self._dev or not t.is_contiguous() or (
+                n is not None and t.numel() != n):
+            raise ValueError(f"{name}: {'' if n is None else n} int32, dense, on {self.device}: "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
     def _rows(self, t, name, shape, dense=True):
-        if t.dtype != self.dtype or t.device != self.device or t.shape != shape:
-            raise ValueError(f"{name}: {self.dtype} {tuple(shape)} on {self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        if dense and not t.is_contiguous():
-            raise ValueError(f"{name} must be dense")
+        if t.dtype is not self.dtype or t.get_device() != self._dev or t.shape != shape or (
+                dense and not t.is_contiguous()):
+            raise ValueError(f"{name}: {self.dtype} {tuple(shape)}{', dense,' if dense else ''} on {self.device}: "
+                             f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
     def _stride(self, t, name):
-        """Elements between a sequence's consecutive tokens; heads and values
-        are dense and sequences follow at the same stride."""
+        """Elements between a sequence's consecutive tokens (0: dense); heads
+        and values are dense and sequences follow at the same stride."""
+        if t.is_contiguous():
+            return 0
         B, T, H, D = t.shape
         s = t.stride()
         token = s[1] if T > 1 else s[0] if B > 1 else H * D
@@ -373,8 +379,17 @@ class KV4Cache:
             raise ValueError(f"{name}: strides {s} are not [tokens * stride, stride, {D}, 1]")
         return token
 
-    def _device(self):
-        return torch.cuda.device(self.device)
+    def _on(self, stream):
+        """(the stream's handle, what makes the cache's device and the stream
+        current, or None where they are)."""
+        if stream is None:
+            return (torch._C._cuda_getCurrentRawStream(self._dev),
+                    None if torch.cuda.current_device() == self._dev else torch.cuda.device(self._dev))
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        if stream.device != self.device:
+            raise ValueError(f"a stream of {stream.device} for a cache on {self.device}")
+        return stream.cuda_stream, torch.cuda.stream(stream)
 
     # ------------------------------------------------------------- calls
 
@@ -383,14 +398,18 @@ class KV4Cache:
         sequence (count[b] of them, or all T).  Rows may be slices of wider
         ones (a fused projection's)."""
         shape = (self.batch, K.shape[1], self.kv_heads, self.head_dim)
-        self._rows(K, "K", shape, dense=False)
-        self._rows(V, "V", shape, dense=False)
+        self._rows(K, "K", shape, False)
+        self._rows(V, "V", shape, False)
         ks, vs = self._stride(K, "K"), self._stride(V, "V")
         self._index(pos, "pos", self.batch)
         if count is not None:
             self._index(count, "count", self.batch)
-        with self._device():
-            abi.sambay_kv4_write(self.abi_cache, self.dims, shape[1], K, V, pos, count, ks, vs, stream)
+        handle, within = self._on(stream)
+        if within is None:
+            abi.sambay_kv4_write(self.abi_cache, self.dims, shape[1], K, V, pos, count, ks, vs, handle)
+        else:
+            with within:
+                abi.sambay_kv4_write(self.abi_cache, self.dims, shape[1], K, V, pos, count, ks, vs, handle)
 
     def read(self, pos, tokens: int, count=None, K=None, V=None, stream=None):
         """The rows K, V [B, tokens, Hkv, dh] that positions pos[b] .. stand
@@ -400,9 +419,20 @@ class KV4Cache:
         self._index(pos, "pos", self.batch)
         if count is not None:
             self._index(count, "count", self.batch)
-        with self._device():
-            K, V = (self._made(t, name, shape, stream, count is not None) for t, name in ((K, "K"), (V, "V")))
-            abi.sambay_kv4_read(self.abi_cache, self.dims, tokens, K, V, pos, count, stream)
+        if K is not None:
+            self._rows(K, "K", shape)
+        if V is not None:
+            self._rows(V, "V", shape)
+        handle, within = self._on(stream)
+        if within is None:
+            return self._read(shape, K, V, pos, count, handle)
+        with within:
+            return self._read(shape, K, V, pos, count, handle)
+
+    def _read(self, shape, K, V, pos, count, handle):
+        K = self._made(shape, count) if K is None else K
+        V = self._made(shape, count) if V is None else V
+        abi.sambay_kv4_read(self.abi_cache, self.dims, shape[1], K, V, pos, count, handle)
         return K, V
 
     def attend(self, q, lens, count=None, scale: float = 0.0, out=None, stream=None):
@@ -410,31 +440,40 @@ class KV4Cache:
         of each sequence's lens[b] cached tokens; q [B, Hq, dh] for one token
         a sequence.  Rows from count[b] on are left as they were (zeros in a
         tensor made here)."""
-        tokens = q.shape[1] if q.dim() == 4 else 1
-        heads = q.shape[-2]
-        shape = (self.batch, tokens, heads, self.head_dim) if q.dim() == 4 else (self.batch, heads, self.head_dim)
+        shape = q.shape
+        plan = self._plans.get(shape)
+        if plan is None:
+            plan = self._plan(shape)
         self._rows(q, "q", shape)
+        if out is not None:
+            self._rows(out, "out", shape)
         self._index(lens, "lens", self.batch)
         if count is not None:
             self._index(count, "count", self.batch)
-        n = self._ws_bytes.get((heads, tokens))
-        if n is None:
-            n = self._ws_bytes[(heads, tokens)] = abi.sambay_cross_attn_decode_kv4_workspace(self.dims, heads, tokens)
-        with self._device():
-            out = self._made(out, "out", shape, stream, count is not None)
-            ws = self._made(None, "ws", (n,), stream, False, torch.uint8) if n else None
-            abi.sambay_cross_attn_decode_kv4(self.abi_cache, self.dims, heads, tokens, q, out, lens, count, scale, ws,
-                                             stream)
+        handle, within = self._on(stream)
+        if within is None:
+            return self._attend(plan, q, lens, count, scale, out, handle)
+        with within:
+            return self._attend(plan, q, lens, count, scale, out, handle)
+
+    def _plan(self, shape):
+        """(query heads, tokens, workspace bytes) for queries of this shape."""
+        if len(shape) not in (3, 4) or shape[0] != self.batch or shape[-1] != self.head_dim:
+            raise ValueError(f"q: [{self.batch}, tokens, heads, {self.head_dim}] or without tokens, got {tuple(shape)}")
+        heads, tokens = shape[-2], shape[1] if len(shape) == 4 else 1
+        plan = heads, tokens, abi.sambay_cross_attn_decode_kv4_workspace(self.dims, heads, tokens)
+        self._plans[shape] = plan
+        return plan
+
+    def _attend(self, plan, q, lens, count, scale, out, handle):
+        heads, tokens, ws_bytes = plan
+        if out is None:
+            out = self._made(q.shape, count)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
+        abi.sambay_cross_attn_decode_kv4(self.abi_cache, self.dims, heads, tokens, q, out, lens, count, scale, ws,
+                                         ws_bytes, handle)
         return out
 
-    def _made(self, t, name, shape, stream, zero, dtype=None):
-        """`t`, checked; or a new tensor that the stream of the call owns."""
-        if t is not None:
-            self._rows(t, name, shape)
-            return t
-        make = torch.zeros if zero else torch.empty
-        if stream is None:
-            return make(shape, dtype=dtype or self.dtype, device=self.device)
-        on = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
-        with torch.cuda.stream(on):
-            return make(shape, dtype=dtype or self.dtype, device=self.device)
+    def _made(self, shape, count):
+        """A new tensor of the current stream (that of the call)."""
+        return (torch.empty if count is None else torch.zeros)(shape, dtype=self.dtype, device=self.device)
