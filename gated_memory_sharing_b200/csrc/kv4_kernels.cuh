@@ -103,8 +103,18 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 __device__ __forceinline__ float2 f16x2_f32(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
-__device__ __forceinline__ uint32_t dup_lo(uint32_t v) { return __byte_perm(v, v, 0x1010); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t v) { return __byte_perm(v, v, 0x3232); }
+// Both halves of `a` times the lower or the upper half of `b` (an operand
+// selection of the multiply, no instruction of its own).
+__device__ __forceinline__ uint32_t mul_f16x2_half(uint32_t a, uint32_t b, int upper) {
+  uint32_t d;
+  if (upper)
+    asm("{\n\t.reg .f16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {h, h};\n\tmul.rn.f16x2 %0, %1, t;\n\t}"
+        : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("{\n\t.reg .f16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {l, l};\n\tmul.rn.f16x2 %0, %1, t;\n\t}"
+        : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 // 8 x 8 of 16 bits, rows over g and columns 2t, 2t + 1, transposed.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
@@ -431,8 +441,7 @@ __device__ __forceinline__ void store_rows(T* p, long long stride, const int (&r
       e2m1x8_f16x2(codes[i][k], x);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t s = e ? dup_hi(sl[k]) : dup_lo(sl[k]);
-        float2 a = f16x2_f32(mul_f16x2(x[2 * e], s)), b = f16x2_f32(mul_f16x2(x[2 * e + 1], s));
+        float2 a = f16x2_f32(mul_f16x2_half(x[2 * e], sl[k], e)), b = f16x2_f32(mul_f16x2_half(x[2 * e + 1], sl[k], e));
         a.x *= two; a.y *= two; b.x *= two; b.y *= two;
         if (row[i] >= 0) store4(p + row[i] * stride + 16 * (2 * k + e) + 4 * t, a, b);
       }
@@ -474,22 +483,22 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const RowParams<T> p) {
 // O) for the combine kernel, which adds them in the line's order.
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 3;
-constexpr int kStageBytes = 4608;
-constexpr int kSmemBytes = kWarps * (kStages * kStageBytes + kStages * 8);
+constexpr int kStages = 2;                       // of a warp's ring,
+constexpr int kStageTiles = 2;                   // two tiles each
+constexpr int kTileBytes = 4608;
+constexpr int kAttnSmem = kWarps * kStages * (kStageTiles * kTileBytes + 8);      // three times this fit an SM
 constexpr long long kWaitCycles = 1LL << 31;     // a copy that has not come after about a second
 // Probabilities are kept times 2^15 (the largest of a row is 2^15): as f16 they
 // then have 11 bits down to 2^-29 of the largest instead of 2^-14, which shows
 // where the likeliest tokens' values are zero.  Numerator and denominator carry
 // the same factor.
 constexpr float kPShift = 15.0f;
+constexpr float kNoRef = 3e38f;                  // the exponent offset of a row that has seen nothing
 
-// Resident CTAs an SM: what the registers of a variant allow (128 registers a
-// thread for 4, 168 for 3, 255 for 2).
-constexpr int attn_ctas(int d, int nt, bool split) {
-  const int size = d * nt * (split ? 2 : 1);
-  return size <= 128 && nt == 1 ? 4 : size <= 256 ? 3 : 2;
-}
+// Resident CTAs an SM: 168 registers a thread suffice for all but the widest
+// variant.  The kernel is bound by what the warp schedulers can dispatch, not
+// by latency: 12, 16 and 20 warps an SM measured the same.
+__host__ __device__ constexpr int attn_ctas(int d, int nt, bool split) { return d * nt * (split ? 2 : 1) <= 256 ? 3 : 2; }
 
 struct AttnParams {
   Pages pg;
@@ -498,9 +507,11 @@ struct AttnParams {
   const int32_t* lens;     // [B] cached tokens, the T new ones among them
   const int32_t* count;    // [B] query tokens of each sequence, or null (T)
   float* o_part;           // [warp][first or last pair][cols, D]  partial outputs
-  float* ml_part;          // [warp][first or last pair][cols, 2]  their (m, l), m in base 2
+  float* ml_part;          // [warp][first or last pair][cols, 2]  their (largest logit, in base 2 and less kPShift; l)
   int T_, Hq, G;
   int row_tiles, cols;     // cols: min(8 NT, G T) columns of a row tile
+  int page_bytes;
+  uint32_t piece_mask, piece_low;      // groups of a page that a stage may hold: a bit each; their number less 1
   int warps;               // of the grid: at most one share of the line each
   float scale_log2;        // scale * log2(e)
 };
@@ -606,70 +617,76 @@ __device__ __forceinline__ int len_of(const AttnParams& p, int b, bool tell) {
 template <int D>
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + 4096 / D - 1) / (4096 / D)); }
 
-// The line: its length in tiles, the warps that share it (none of them without
-// a tile), and where share w begins.
+// The line: its length in tiles (below 2^31, the host sees to it) and the warps
+// that share it, none of them without a tile: share w has `base` tiles, or one
+// more (the first `rem` of them).
 struct Line {
-  long long tiles;
-  int shares;
-  __device__ __forceinline__ long long begin(long long w) const { return tiles * w / shares; }
+  int shares, base, rem;
+  __device__ __forceinline__ int begin(int w) const { return w * base + min(w, rem); }
   // the share that holds tile x
-  __device__ __forceinline__ int share_of(long long x) const {
-    return static_cast<int>(((x + 1) * shares - 1) / tiles);
+  __device__ __forceinline__ int share_of(int x) const {
+    const int cut = rem * (base + 1);
+    return x < cut ? x / (base + 1) : rem + (x - cut) / base;
   }
 };
 
 // The line of a call, and the tile in it at which sequence b begins (one warp).
 template <int D>
-__device__ __forceinline__ Line line_of(const AttnParams& p, int b, bool tell, long long* before) {
-  long long s = 0, sb = 0;
+__device__ __forceinline__ Line line_of(const AttnParams& p, int b, bool tell, int* before) {
+  int s = 0, sb = 0;
   for (int i = threadIdx.x & 31; i < p.pg.B; i += 32) {
     const int n = tiles_of<D>(len_of(p, i, tell));
     s += n;
     if (i < b) sb += n;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    sb += __shfl_xor_sync(0xFFFFFFFFu, sb, o);
-  }
-  *before = sb * p.pg.Hkv * p.row_tiles;
+  s = __reduce_add_sync(0xFFFFFFFFu, s);
+  sb = __reduce_add_sync(0xFFFFFFFFu, sb);
+  const int pairs = p.pg.Hkv * p.row_tiles;
+  *before = sb * pairs;
   Line line;
-  line.tiles = s * p.pg.Hkv * p.row_tiles;
-  line.shares = static_cast<int>(min(line.tiles, static_cast<long long>(p.warps)));
+  line.shares = min(s * pairs, p.warps);
+  line.base = s * pairs / line.shares;
+  line.rem = s * pairs - line.base * line.shares;
   return line;
 }
 
 // A place in the line.
 struct Cursor {
-  int b, pair, tile;       // pair: KV head * row tiles + row tile
+  int b, h, rt, tile;      // sequence, KV head, row tile, tile
   int len, tiles;          // of sequence b
 };
 
+// n tiles on (no further than the pair's end); true if that is another pair.
 template <int D>
-__device__ __forceinline__ void advance(const AttnParams& p, Cursor& c) {
-  if (++c.tile < c.tiles) return;
+__device__ __forceinline__ bool advance(const AttnParams& p, Cursor& c, int n) {
+  if ((c.tile += n) < c.tiles) return false;
   c.tile = 0;
-  if (++c.pair < p.pg.Hkv * p.row_tiles) return;
-  c.pair = 0;
-  if (++c.b < p.pg.B) {
-    c.len = len_of(p, c.b, false);
-    c.tiles = tiles_of<D>(c.len);
+  if (++c.rt == p.row_tiles) {
+    c.rt = 0;
+    if (++c.h == p.pg.Hkv) {
+      c.h = 0;
+      if (++c.b < p.pg.B) {
+        c.len = len_of(p, c.b, false);
+        c.tiles = tiles_of<D>(c.len);
+      }
+    }
   }
+  return true;
 }
 
 // Tile x of the line.
 template <int D>
-__device__ __forceinline__ Cursor find(const AttnParams& p, long long x) {
+__device__ __forceinline__ Cursor find(const AttnParams& p, int x) {
   const int lane = threadIdx.x & 31;
   const int pairs = p.pg.Hkv * p.row_tiles;
   Cursor c{};
   for (int b0 = 0; b0 < p.pg.B; b0 += 32) {
     const int len = b0 + lane < p.pg.B ? len_of(p, b0 + lane, false) : 0;
     const int n = b0 + lane < p.pg.B ? tiles_of<D>(len) : 0;
-    long long upto = static_cast<long long>(n) * pairs;            // of this and the sequences before it
+    int upto = n * pairs;                                          // of this and the sequences before it
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
       if (lane >= o) upto += v;
     }
     const unsigned past = __ballot_sync(0xFFFFFFFFu, upto > x);
@@ -678,9 +695,11 @@ __device__ __forceinline__ Cursor find(const AttnParams& p, long long x) {
       c.b = b0 + k;
       c.len = __shfl_sync(0xFFFFFFFFu, len, k);
       c.tiles = __shfl_sync(0xFFFFFFFFu, n, k);
-      const long long in = x - (__shfl_sync(0xFFFFFFFFu, upto, k) - static_cast<long long>(c.tiles) * pairs);
-      c.pair = static_cast<int>(in / c.tiles);
-      c.tile = static_cast<int>(in % c.tiles);
+      const int in = x - (__shfl_sync(0xFFFFFFFFu, upto, k) - c.tiles * pairs);
+      const int pair = in / c.tiles;
+      c.tile = in - pair * c.tiles;
+      c.h = pair / p.row_tiles;
+      c.rt = pair - c.h * p.row_tiles;
       return c;
     }
     x -= __shfl_sync(0xFFFFFFFFu, upto, 31);
@@ -697,83 +716,88 @@ template <typename T, int D, int NT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_kernel(const AttnParams p) {
   constexpr int KS = D / 16;
   constexpr int NQ = SPLIT ? 2 : 1;
-  constexpr int TILE = 4096 / D, GP = TILE / kGroup;
+  constexpr int TILE = 4096 / D, GP = TILE / kGroup, WIN = 32 / GP;     // WIN: tiles of 32 groups
+  constexpr int SG = kStageTiles * GP;                                  // groups of a stage
+  constexpr int S = kStages, kStageBytes = kStageTiles * kTileBytes;
   extern __shared__ __align__(128) uint8_t smem[];
+  pdl_launch_dependents();             // the combine kernel's CTAs come as this one's leave
   const Pages& pg = p.pg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   // the first warps of all CTAs, then their second ones: few shares spread over the GPU
   const int gw = warp * gridDim.x + blockIdx.x;
-  uint8_t* ring = smem + warp * (kStages * kStageBytes);
+  uint8_t* ring = smem + warp * (S * kStageBytes);
   const uint32_t ring_addr = shared_addr(ring);
-  const uint32_t bars = shared_addr(smem + kWarps * kStages * kStageBytes) + warp * (kStages * 8);
+  const uint32_t bars = shared_addr(smem + kWarps * S * kStageBytes) + warp * (S * 8);
 
-  long long none;
+  int none;
   const Line line = line_of<D>(p, 0, gw == 0, &none);
   if (gw >= line.shares) return;
-  const long long begin = line.begin(gw);
-  const int share = static_cast<int>(line.begin(gw + 1) - begin);
-  if (lane < kStages) bar_init(bars + 8 * lane);
+  const int begin = line.begin(gw), share = line.begin(gw + 1) - begin;
+  if (lane < S) bar_init(bars + 8 * lane);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
 
-  Cursor in = find<D>(p, begin);       // the next tile to load
-  Cursor c = in;                       // the tile being worked on
+  Cursor c = find<D>(p, begin);        // the tile being worked on
+  Cursor in = c;                       // the next tile to load
 
-  // Pages of the 32 groups of the loading cursor's window (512 tokens), one a lane.
-  int win_b = -1, win = -1, page = -1;
-  uint32_t have = 0;                   // GP bits a stage: which groups were loaded
+  // Pages of the 32 groups of the loading cursor's window, one a lane.
+  int page = -1;
+  bool window = true;                  // to be loaded
+  uint32_t have = 0;                   // SG bits a stage: which groups were loaded
+  int loaded = 0;                      // tiles of the share that are on their way or here
+  // The tiles that a stage takes at a place: two of one pair, from an even one on.
+  auto step_of = [&](const Cursor& x, int left) {
+    return (x.tile & 1) ? 1 : min(min(kStageTiles, left), x.tiles - x.tile);
+  };
   auto issue = [&](int st) {
-    const int tok0 = in.tile * TILE;
-    if (in.b != win_b || (tok0 >> 9) != win) {
-      win_b = in.b;
-      win = tok0 >> 9;
-      const int tok = win * 512 + lane * kGroup;
+    const int n = step_of(in, share - loaded);
+    const int tok = in.tile * TILE + lane * kGroup;
+    if (window || in.tile % WIN == 0) {
+      window = false;
+      const int first = tok - in.tile % WIN * TILE;
       page = -1;
-      if (tok < in.len) {
-        page = pg.table[static_cast<long long>(in.b) * pg.table_pages + (tok >> pg.page_log2)];
+      if (first < in.len) {
+        page = pg.table[static_cast<long long>(in.b) * pg.table_pages + (first >> pg.page_log2)];
         if (page < 0 || page >= pg.num_pages) {
           page = -1;
           record_status(kStatusBadIndex);
         }
       }
     }
-    // lane q: group q of the tile
-    const int pid = __shfl_sync(0xFFFFFFFFu, page, (tok0 >> 4) + lane);
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lane < GP && pid >= 0);
-    const int h = in.pair / p.row_tiles;
-    const int at = ((tok0 + lane * kGroup) & ((1 << pg.page_log2) - 1)) / kGroup;
-    const uint8_t* src =
-        pg.cache + (((static_cast<long long>(pid) * pg.Hkv + h) << (pg.page_log2 - 4)) + at) * Block<D>::kBytes;
-    const uint32_t dst = ring_addr + st * kStageBytes, bar = bars + 8 * st;
+    // lane q: group q of the stage
+    const int pid = __shfl_sync(0xFFFFFFFFu, page, in.tile % WIN * GP + lane);
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lane < n * GP && pid >= 0);
+    const int at = (in.h << (pg.page_log2 - 4)) + ((tok & ((1 << pg.page_log2) - 1)) / kGroup);   // group of the page
+    const uint8_t* src = pg.cache + static_cast<long long>(pid) * p.page_bytes + at * Block<D>::kBytes;
+    const uint32_t bar = bars + 8 * st;
     if (lane == 0) bar_expect(bar, __popc(mask) * Block<D>::kBytes);
-    if ((1 << pg.page_log2) >= TILE) {               // one piece: the groups below the sequence's end
-      if (lane == 0 && mask) bulk_load(dst, src, __popc(mask) * Block<D>::kBytes, bar);
-    } else if (mask >> lane & 1) {
-      bulk_load(dst + lane * Block<D>::kBytes, src, Block<D>::kBytes, bar);
-    }
-    have = (have & ~(((1u << GP) - 1) << (GP * st))) | mask << (GP * st);
-    advance<D>(p, in);
+    // what lies in one page is one piece (its groups below the sequence's end)
+    const uint32_t piece = (mask >> lane) & p.piece_mask;
+    if (piece && (lane & p.piece_low) == 0)
+      bulk_load(ring_addr + st * kStageBytes + lane * Block<D>::kBytes, src, __popc(piece) * Block<D>::kBytes, bar);
+    have = (have & ~(((1u << SG) - 1) << (SG * st))) | mask << (SG * st);
+    loaded += n;
+    window = advance<D>(p, in, n);
   };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i)
-    if (i < share) issue(i);
+  issue(0);
 
   uint32_t qb[NQ][NT][KS][2];
   float f[NT][2];
   int lim[NT][2];
-  float m[NT][2], ref[NT][2], l[NT][2], o[NT][KS][4];      // ref: what exponents are relative to
+  float ref[NT][2], l[NT][2], o[NT][KS][4];
   bool fresh = true;
   int st = 0, lim_min = 0;
   uint32_t parity = 0;
 
-  for (int i = 0; i < share; ++i) {
-    if (i + kStages - 1 < share) issue(st == 0 ? kStages - 1 : st - 1);
+  for (int i = 0; i < share;) {        // i: tiles done
+    const int n = step_of(c, share - i);
+    if (loaded < share) issue(st ^ 1);
     if (fresh) {
       // B fragments of Q (column g of n-tile n), and per accumulator column its factor and its last token
       fresh = false;
-      const int h = c.pair / p.row_tiles, row0 = c.pair % p.row_tiles * (8 * NT);
-      const int nq = rows_of(p.count, c.b, p.T_, c.pair == 0);
+      const int h = c.h, row0 = c.rt * (8 * NT);
+      const int nq = rows_of(p.count, c.b, p.T_, h == 0 && row0 == 0);
       lim_min = c.len;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -823,8 +847,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
         for (int e = 0; e < 2; ++e) {
           f[n][e] = __shfl_sync(0xFFFFFFFFu, fac, (2 * t + e) * 4);
           lim[n][e] = min(c.len, __shfl_sync(0xFFFFFFFFu, limit, (2 * t + e) * 4));
-          m[n][e] = -INFINITY;
-          ref[n][e] = 0.0f;
+          ref[n][e] = kNoRef;
           l[n][e] = 0.0f;
         }
 #pragma unroll
@@ -832,229 +855,206 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
       }
       lim_min = __reduce_min_sync(0xFFFFFFFFu, lim_min);
     }
-    if (!bar_wait(bars + 8 * st, parity)) {
+    if (!bar_wait(bars + 8 * st, parity >> st & 1)) {
       // lost: tell, and leave when the copies in flight have come (or again do not)
       record_status(kStatusTimeout);
-      for (int k = i; k < min(share, i + kStages); ++k) {
-        bar_wait(bars + 8 * st, parity);
-        if (++st == kStages) st = 0, parity ^= 1;
-      }
+      bar_wait(bars + 8 * st, parity >> st & 1);
+      if (i + n < loaded) bar_wait(bars + 8 * (st ^ 1), parity >> (st ^ 1) & 1);
       return;
     }
+    parity ^= 1u << st;
 
-    const int tok0 = c.tile * TILE;
-    const uint32_t mask = have >> (GP * st) & ((1u << GP) - 1);
+    const uint32_t mask = have >> (SG * st) & ((1u << SG) - 1);
     const uint8_t* stage = ring + st * kStageBytes;
-    float s[NT][GP][4];
-    // S^T of group q: entries 0, 1: token g, columns 2t, 2t + 1; entries 2, 3: token g + 8
-    auto scores = [&](int q) {
-      const uint8_t* grp = stage + q * Block<D>::kBytes;
-      uint32_t kc[KS], sc[2][KS / 4];
+    // One tile.  EDGE: not every column sees all of its tokens, or some are missing.
+    auto tile = [&](int tok0, const uint8_t* base, uint32_t here, auto edge) {
+      constexpr bool EDGE = decltype(edge)::value;
+      // S^T of group q: entries 0, 1: token g, columns 2t, 2t + 1; entries 2, 3: token g + 8
+      float s[NT][GP][4];
 #pragma unroll
-      for (int k = 0; k < KS / 4; ++k) {
-        const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kK + k * 512 + lane * 16);
-        kc[4 * k] = v.x; kc[4 * k + 1] = v.y; kc[4 * k + 2] = v.z; kc[4 * k + 3] = v.w;
+      for (int q = 0; q < GP; ++q) {
+        const uint8_t* grp = base + q * Block<D>::kBytes;
+        if (!EDGE || (here >> q & 1)) {
+          uint32_t kc[KS], sc[2][KS / 4];
+#pragma unroll
+          for (int k = 0; k < KS / 4; ++k) {
+            const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kK + k * 512 + lane * 16);
+            kc[4 * k] = v.x; kc[4 * k + 1] = v.y; kc[4 * k + 2] = v.z; kc[4 * k + 3] = v.w;
+          }
+          if (KS == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(grp + Block<D>::kKs + g * 8);
+            sc[0][0] = v.x; sc[1][0] = v.y;
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kKs + g * 16);
+            sc[0][0] = v.x; sc[0][KS / 4 - 1] = v.y; sc[1][0] = v.z; sc[1][KS / 4 - 1] = v.w;
+          }
+#pragma unroll
+          for (int k = 0; k < KS / 4; ++k) {
+            uint32_t sl[2][2];
+            e4m3x4_f16x2(sc[0][k], sl[0][0], sl[0][1]);
+            e4m3x4_f16x2(sc[1][k], sl[1][0], sl[1][1]);
+#pragma unroll
+            for (int bp = 0; bp < 2; ++bp) {           // blocks 4k + 2 bp, + 1
+              uint32_t x0[4], x1[4];                   // tokens g and g + 8
+              e2m1x8_f16x2(kc[4 * k + bp], x0);
+              e2m1x8_f16x2(kc[4 * k + 2 + bp], x1);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t a0 = mul_f16x2_half(x0[2 * e], sl[0][bp], e), a1 = mul_f16x2_half(x1[2 * e], sl[1][bp], e);
+                const uint32_t a2 = mul_f16x2_half(x0[2 * e + 1], sl[0][bp], e), a3 = mul_f16x2_half(x1[2 * e + 1], sl[1][bp], e);
+                const int kb = 4 * k + 2 * bp + e;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  if (kb == 0)
+                    mma16816_f16_zero(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
+                  else
+                    mma16816_f16(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
+                  if (SPLIT) mma16816_f16(s[n][q], a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
+                }
+              }
+            }
+          }
+        }
+        if (EDGE) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!(here >> q & 1) || tok0 + q * kGroup + g + 8 * (e >> 1) >= lim[n][e & 1]) s[n][q][e] = -INFINITY;
+        }
       }
-      if (KS == 4) {
-        const uint2 v = *reinterpret_cast<const uint2*>(grp + Block<D>::kKs + g * 8);
-        sc[0][0] = v.x; sc[1][0] = v.y;
-      } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kKs + g * 16);
-        sc[0][0] = v.x; sc[0][KS / 4 - 1] = v.y; sc[1][0] = v.z; sc[1][KS / 4 - 1] = v.w;
-      }
+      // online softmax per column: p = 2^(f s + ref), f > 0, ref = kPShift less the
+      // largest logit so far; most tiles hold no larger one
+      bool grown = false;
+      float mx[NT][2];
 #pragma unroll
-      for (int k = 0; k < KS / 4; ++k) {
-        uint32_t sl[2][2];
-        e4m3x4_f16x2(sc[0][k], sl[0][0], sl[0][1]);
-        e4m3x4_f16x2(sc[1][k], sl[1][0], sl[1][1]);
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int bp = 0; bp < 2; ++bp) {             // blocks 4k + 2 bp, + 1
-          uint32_t x0[4], x1[4];                     // tokens g and g + 8
-          e2m1x8_f16x2(kc[4 * k + bp], x0);
-          e2m1x8_f16x2(kc[4 * k + 2 + bp], x1);
-          const float2 f0 = f16x2_f32(sl[0][bp]), f1 = f16x2_f32(sl[1][bp]);
+        for (int e = 0; e < 2; ++e) {
+          mx[n][e] = fmaxf(s[n][0][e], s[n][0][e + 2]);
+#pragma unroll
+          for (int q = 1; q < GP; ++q) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[n][q][e], s[n][q][e + 2]));
+          grown |= fmaf(mx[n][e], f[n][e], ref[n][e]) > kPShift;
+        }
+      if (__any_sync(0xFFFFFFFFu, grown)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float corr[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int kb = 4 * k + 2 * bp + e;
-            if (NT == 1) {
-              // the block's scales on its products: 4 operations, as many as on
-              // the codes, but none on the pipe that converts them
-              float d[4];
-              mma16816_f16_zero(d, x0[2 * e], x1[2 * e], x0[2 * e + 1], x1[2 * e + 1], qb[0][0][kb][0], qb[0][0][kb][1]);
-              if (SPLIT)
-                mma16816_f16(d, x0[2 * e], x1[2 * e], x0[2 * e + 1], x1[2 * e + 1], qb[NQ - 1][0][kb][0], qb[NQ - 1][0][kb][1]);
-              const float s0 = e ? f0.y : f0.x, s1 = e ? f1.y : f1.x;
-              s[0][q][0] = kb == 0 ? d[0] * s0 : fmaf(d[0], s0, s[0][q][0]);
-              s[0][q][1] = kb == 0 ? d[1] * s0 : fmaf(d[1], s0, s[0][q][1]);
-              s[0][q][2] = kb == 0 ? d[2] * s1 : fmaf(d[2], s1, s[0][q][2]);
-              s[0][q][3] = kb == 0 ? d[3] * s1 : fmaf(d[3], s1, s[0][q][3]);
-            } else {
-              const uint32_t s0 = e ? dup_hi(sl[0][bp]) : dup_lo(sl[0][bp]);
-              const uint32_t s1 = e ? dup_hi(sl[1][bp]) : dup_lo(sl[1][bp]);
-              const uint32_t a0 = mul_f16x2(x0[2 * e], s0), a1 = mul_f16x2(x1[2 * e], s1);
-              const uint32_t a2 = mul_f16x2(x0[2 * e + 1], s0), a3 = mul_f16x2(x1[2 * e + 1], s1);
+            float x = mx[n][e];
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+            const float to = fminf(ref[n][e], kPShift - x * f[n][e]);
+            corr[e] = ex2_approx(to - ref[n][e]);          // 0 from kNoRef
+            ref[n][e] = to;
+            l[n][e] *= corr[e];
+          }
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                if (kb == 0)
-                  mma16816_f16_zero(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
-                else
-                  mma16816_f16(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
-                if (SPLIT) mma16816_f16(s[n][q], a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
+          for (int k = 0; k < KS; ++k) {
+            const float2 u = mul2(make_float2(o[n][k][0], o[n][k][1]), make_float2(corr[0], corr[1]));
+            const float2 v = mul2(make_float2(o[n][k][2], o[n][k][3]), make_float2(corr[0], corr[1]));
+            o[n][k][0] = u.x; o[n][k][1] = u.y; o[n][k][2] = v.x; o[n][k][3] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < GP; ++q) {
+        if (EDGE && !(here >> q & 1)) continue;
+        const uint8_t* grp = base + q * Block<D>::kBytes;
+        const int tok = tok0 + q * kGroup;
+        uint32_t pb[NQ][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float2 fn = make_float2(f[n][0], f[n][1]), rn = make_float2(ref[n][0], ref[n][1]);
+          const float2 u = fma2(make_float2(s[n][q][0], s[n][q][1]), fn, rn);
+          const float2 v = fma2(make_float2(s[n][q][2], s[n][q][3]), fn, rn);
+          const float2 pu = make_float2(ex2_approx(u.x), ex2_approx(u.y)), pv = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+          const float2 ln = add2(make_float2(l[n][0], l[n][1]), add2(pu, pv));
+          l[n][0] = ln.x;
+          l[n][1] = ln.y;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 pe = e ? pv : pu;
+            const uint32_t hi = pack_f16(pe.x, pe.y);
+            pb[0][n][e] = movmatrix_trans(hi);
+            if (SPLIT) {
+              const float2 h2 = f16x2_f32(hi);
+              pb[NQ - 1][n][e] = movmatrix_trans(pack_f16(pe.x - h2.x, pe.y - h2.y));
+            }
+          }
+        }
+        // O^T += V^T P^T.  At an edge the scales of tokens that are not the
+        // sequence's are blanked, whose P is 0 (0 x NaN is not), and a block of
+        // NaN reaches only the columns that see its token: its scale is blanked
+        // too, and these columns are set to NaN.
+        uint32_t keep = 0xFFFFFFFFu;
+        if (EDGE) {
+          keep = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (tok + 2 * t + (e & 1) + 8 * (e >> 1) < c.len) keep |= 0xFFu << (8 * e);
+        }
+#pragma unroll
+        for (int k = 0; k < KS / 4; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kV + k * 512 + lane * 16);
+          const uint4 sv = *reinterpret_cast<const uint4*>(grp + Block<D>::kVs + t * (D / 4) + k * 16);
+          uint32_t scw[4] = {sv.x & keep, sv.y & keep, sv.z & keep, sv.w & keep};
+          uint32_t x0[4], x1[4], x2[4], x3[4];
+          e2m1x8_f16x2(v.x, x0);       // values 2g, tokens 2t, 2t + 1
+          e2m1x8_f16x2(v.y, x1);       // values 2g + 1
+          e2m1x8_f16x2(v.z, x2);       // values 2g, tokens 2t + 8, 2t + 9
+          e2m1x8_f16x2(v.w, x3);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            int bad = 0x7FFFFFFF;                     // first token of the group whose block is NaN
+            if (EDGE) {
+              const uint32_t nan = __vcmpeq4(scw[e], 0x7F7F7F7Fu);
+              if (__any_sync(0xFFFFFFFFu, nan != 0)) {
+                scw[e] &= ~nan;
+                if (nan) bad = tok + 2 * t + (nan & 0xFFu ? 0 : nan & 0xFF00u ? 1 : nan & 0xFF0000u ? 8 : 9);
+                bad = min(bad, __shfl_xor_sync(0xFFFFFFFFu, bad, 1));
+                bad = min(bad, __shfl_xor_sync(0xFFFFFFFFu, bad, 2));
+              }
+            }
+            uint32_t slo, shi;
+            e4m3x4_f16x2(scw[e], slo, shi);
+            const uint32_t a0 = mul_f16x2(x0[e], slo), a1 = mul_f16x2(x1[e], slo);
+            const uint32_t a2 = mul_f16x2(x2[e], shi), a3 = mul_f16x2(x3[e], shi);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
+              if (SPLIT) mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[NQ - 1][n][0], pb[NQ - 1][n][1]);
+              if (EDGE) {
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2)
+                  if (bad < lim[n][i2 & 1]) o[n][4 * k + e][i2] = __int_as_float(0x7FC00000);
               }
             }
           }
         }
       }
     };
-    // O^T += V^T P^T of group q.  Where not all see all (EDGE): the bytes of
-    // `keep` that are 0 blank the scales of tokens that are not the sequence's,
-    // whose P is 0 (0 x NaN is not), and a block of NaN reaches only the columns
-    // that see its token: its scale is blanked too, and the columns set to NaN.
-    auto outputs = [&](int q, uint32_t keep, auto edge) {
-      constexpr bool EDGE = decltype(edge)::value;
-      const uint8_t* grp = stage + q * Block<D>::kBytes;
-      uint32_t pb[NQ][NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t hi = pack_f16(s[n][q][2 * e], s[n][q][2 * e + 1]);
-          pb[0][n][e] = movmatrix_trans(hi);
-          if (SPLIT) {
-            const float2 h2 = f16x2_f32(hi);
-            pb[NQ - 1][n][e] = movmatrix_trans(pack_f16(s[n][q][2 * e] - h2.x, s[n][q][2 * e + 1] - h2.y));
-          }
-        }
-#pragma unroll
-      for (int k = 0; k < KS / 4; ++k) {
-        const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kV + k * 512 + lane * 16);
-        const uint4 sv = *reinterpret_cast<const uint4*>(grp + Block<D>::kVs + t * (D / 4) + k * 16);
-        uint32_t scw[4] = {sv.x & keep, sv.y & keep, sv.z & keep, sv.w & keep};
-        uint32_t x0[4], x1[4], x2[4], x3[4];
-        e2m1x8_f16x2(v.x, x0);         // values 2g, tokens 2t, 2t + 1
-        e2m1x8_f16x2(v.y, x1);         // values 2g + 1
-        e2m1x8_f16x2(v.z, x2);         // values 2g, tokens 2t + 8, 2t + 9
-        e2m1x8_f16x2(v.w, x3);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          int bad = 0x7FFFFFFF;                       // first token of the group whose block is NaN
-          if (EDGE) {
-            const uint32_t nan = __vcmpeq4(scw[e], 0x7F7F7F7Fu);
-            if (__any_sync(0xFFFFFFFFu, nan != 0)) {
-              scw[e] &= ~nan;
-              if (nan) bad = tok0 + q * kGroup + 2 * t + (nan & 0xFFu ? 0 : nan & 0xFF00u ? 1 : nan & 0xFF0000u ? 8 : 9);
-              bad = min(bad, __shfl_xor_sync(0xFFFFFFFFu, bad, 1));
-              bad = min(bad, __shfl_xor_sync(0xFFFFFFFFu, bad, 2));
-            }
-          }
-          uint32_t slo, shi;
-          e4m3x4_f16x2(scw[e], slo, shi);
-          const uint32_t a0 = mul_f16x2(x0[e], slo), a1 = mul_f16x2(x1[e], slo);
-          const uint32_t a2 = mul_f16x2(x2[e], shi), a3 = mul_f16x2(x3[e], shi);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
-            if (SPLIT) mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[NQ - 1][n][0], pb[NQ - 1][n][1]);
-            if (EDGE) {
-#pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2)
-                if (bad < lim[n][i2 & 1]) o[n][4 * k + e][i2] = __int_as_float(0x7FC00000);
-            }
-          }
-        }
-      }
-    };
-    const bool whole = mask == (1u << GP) - 1 && tok0 + TILE <= lim_min;   // every column sees every token
-    if (whole) {
-#pragma unroll
-      for (int q = 0; q < GP; ++q) scores(q);
-    } else {
-#pragma unroll
-      for (int q = 0; q < GP; ++q) {
-        if (mask >> q & 1) scores(q);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!(mask >> q & 1) || tok0 + q * kGroup + g + 8 * (e >> 1) >= lim[n][e & 1]) s[n][q][e] = -INFINITY;
-      }
-    }
-    // online softmax per column: the factor f > 0, so the largest s is the largest logit
-    float mx[NT][2];
-    bool grown = false;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[n][e] = fmaxf(s[n][0][e], s[n][0][e + 2]);
-#pragma unroll
-        for (int q = 1; q < GP; ++q) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[n][q][e], s[n][q][e + 2]));
-        mx[n][e] *= f[n][e];
-        grown |= mx[n][e] > m[n][e];
-      }
-    if (__any_sync(0xFFFFFFFFu, grown)) {      // most tiles hold no new maximum
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float corr[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = mx[n][e];
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-          const float mn = fmaxf(m[n][e], x);
-          corr[e] = mn == -INFINITY ? 0.0f : ex2_approx(m[n][e] - mn);
-          m[n][e] = mn;
-          ref[n][e] = mn == -INFINITY ? 0.0f : kPShift - mn;        // a column that sees none of these tokens
-          l[n][e] *= corr[e];
-        }
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const float2 u = mul2(make_float2(o[n][k][0], o[n][k][1]), make_float2(corr[0], corr[1]));
-          const float2 v = mul2(make_float2(o[n][k][2], o[n][k][3]), make_float2(corr[0], corr[1]));
-          o[n][k][0] = u.x; o[n][k][1] = u.y; o[n][k][2] = v.x; o[n][k][3] = v.y;
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float2 fn = make_float2(f[n][0], f[n][1]), rn = make_float2(ref[n][0], ref[n][1]);
-      float2 ln = make_float2(l[n][0], l[n][1]);
-#pragma unroll
-      for (int q = 0; q < GP; ++q) {
-        const float2 u = fma2(make_float2(s[n][q][0], s[n][q][1]), fn, rn);
-        const float2 v = fma2(make_float2(s[n][q][2], s[n][q][3]), fn, rn);
-        s[n][q][0] = ex2_approx(u.x); s[n][q][1] = ex2_approx(u.y);
-        s[n][q][2] = ex2_approx(v.x); s[n][q][3] = ex2_approx(v.y);
-        ln = add2(ln, add2(make_float2(s[n][q][0], s[n][q][1]), make_float2(s[n][q][2], s[n][q][3])));
-      }
-      l[n][0] = ln.x;
-      l[n][1] = ln.y;
-    }
-    if (whole) {
-#pragma unroll
-      for (int q = 0; q < GP; ++q) outputs(q, 0xFFFFFFFFu, std::false_type());
-    } else {
-#pragma unroll
-      for (int q = 0; q < GP; ++q) {
-        const int left = c.len - (tok0 + q * kGroup);
-        uint32_t keep = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (2 * t + (e & 1) + 8 * (e >> 1) < left) keep |= 0xFFu << (8 * e);
-        if (mask >> q & 1) outputs(q, keep, std::true_type());
-      }
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+      const int tok0 = (c.tile + k) * TILE;
+      const uint32_t here = mask >> (GP * k) & ((1u << GP) - 1);
+      if (here == (1u << GP) - 1 && tok0 + TILE <= lim_min)
+        tile(tok0, stage + k * kTileBytes, here, std::false_type());
+      else
+        tile(tok0, stage + k * kTileBytes, here, std::true_type());
     }
     __syncwarp();                      // the stage is read; the next iteration's copies may refill it
-    if (++st == kStages) st = 0, parity ^= 1;
+    st ^= 1;
 
-    if (c.tile + 1 == c.tiles || i + 1 == share) {
+    if (c.tile + n == c.tiles || i + n == share) {
       // the pair, or this warp's share of it, is done
-      const int h = c.pair / p.row_tiles, row0 = c.pair % p.row_tiles * (8 * NT);
+      const int h = c.h, row0 = c.rt * (8 * NT);
       const int nq = rows_of(p.count, c.b, p.T_, false);
       const float ve = pow2i(head_exp(pg.v_exp, h));
       const bool from_start = i >= c.tile;                     // the pair's first tile is in this share
-      const bool done = from_start && c.tile + 1 == c.tiles;
+      const bool done = from_start && c.tile + n == c.tiles;
       // the share's first pair leaves its part in slot 0, its last one in slot 1
       const long long slot = static_cast<long long>(gw) * 2 + (i == c.tile || !from_start ? 0 : 1);
 #pragma unroll
@@ -1077,13 +1077,14 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
               float* dst = p.o_part + (slot * p.cols + col) * D;
 #pragma unroll
               for (int k = 0; k < KS; ++k) store2(dst + 16 * k + 2 * g, o[n][k][e], o[n][k][e + 2]);
-              if (g == 0) store2(p.ml_part + (slot * p.cols + col) * 2, m[n][e], ls);
+              if (g == 0) store2(p.ml_part + (slot * p.cols + col) * 2, -ref[n][e], ls);
             }
           }
         }
       fresh = true;
     }
-    advance<D>(p, c);
+    advance<D>(p, c, n);
+    i += n;
   }
 }
 
@@ -1092,29 +1093,30 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
 template <typename T, int D, int NT, int WARPS>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
   constexpr int V = D / 32;            // values a lane
-  pdl_wait();
   const Pages& pg = p.pg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row = WARPS == 1 ? blockIdx.x * 8LL + warp : blockIdx.x;
-  if (row >= static_cast<long long>(pg.B) * p.T_ * p.Hq) return;
-  const int hq = static_cast<int>(row % p.Hq);
-  const int tok = static_cast<int>(row / p.Hq % p.T_), b = static_cast<int>(row / p.Hq / p.T_);
-  if (tok >= rows_of(p.count, b, p.T_, false)) return;
+  const bool in = row < static_cast<long long>(pg.B) * p.T_ * p.Hq;
+  const int hq = in ? static_cast<int>(row % p.Hq) : 0;
+  const int tok = in ? static_cast<int>(row / p.Hq % p.T_) : 0, b = in ? static_cast<int>(row / p.Hq / p.T_) : 0;
+  const bool live = in && tok < rows_of(p.count, b, p.T_, false);
   const int h = hq / p.G, r = tok * p.G + hq % p.G;
   const int pair = h * p.row_tiles + r / (8 * NT), col = r % (8 * NT);
-  long long before;
+  int before;
   const Line line = line_of<D>(p, b, false, &before);
   const int tiles = tiles_of<D>(len_of(p, b, false));
-  const long long a = before + static_cast<long long>(pair) * tiles;
+  const int a = before + pair * tiles;
   const int w0 = line.share_of(a), w1 = line.share_of(a + tiles - 1);
-  if (w0 == w1) return;                // finished by that warp
   const int first = line.begin(w0) == a ? 0 : 1;
+  // what was read so far no kernel of this call writes; every thread waits, so
+  // that this kernel does not end before the one whose parts it reads
+  pdl_wait();
+  if (!live || w0 == w1) return;       // w0 == w1: finished by that warp
   auto slot = [&](int w) { return (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col; };
-  float ms = -INFINITY;
+  float ms = -kNoRef;
   for (int w = w0 + lane; w <= w1; w += 32) ms = fmaxf(ms, p.ml_part[slot(w) * 2]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xFFFFFFFFu, ms, o));
-  const float ref = ms == -INFINITY ? 0.0f : ms;
   float num[V], den = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) num[v] = 0.0f;
@@ -1125,7 +1127,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
   for (int w = lo; w < hi; ++w) {
     const long long k = slot(w);
     const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + k * 2);
-    const float fw = ex2_approx(ml.x - ref);
+    const float fw = ex2_approx(ml.x - ms);
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
       float x[2];

@@ -1600,6 +1600,8 @@ sambay_status kv4_check(const sambay_kv4_dims* d) {
   if (d->page_tokens < 16 || d->page_tokens > 1024 || (d->page_tokens & (d->page_tokens - 1)) != 0)
     return SAMBAY_ERR_UNSUPPORTED;
   if (static_cast<long long>(d->table_pages) * d->page_tokens > (1LL << 30)) return SAMBAY_ERR_UNSUPPORTED;
+  if (static_cast<long long>(d->kv_heads) * (d->page_tokens / 16) * 18 * d->head_dim > (1LL << 30))
+    return SAMBAY_ERR_UNSUPPORTED;                       // a page of over 1 GB
   if (d->kv_heads > 65535 || d->batch > 65535) return SAMBAY_ERR_UNSUPPORTED;
   return SAMBAY_OK;
 }
@@ -1676,7 +1678,7 @@ constexpr int kKv4MaxTokens = 16;
 // resident CTAs, or fewer where the table has room for fewer tiles; and the
 // parts that each warp may leave of its first and its last pair.
 struct Kv4Plan {
-  int nt = 1, row_tiles = 1, cols = 8, grid = 1;
+  int nt = 1, row_tiles = 1, cols = 8, grid = 0;
   bool one_tile = false;       // no pair has more than one tile: nothing is shared
   bool many = false;           // about how many parts a pair has
   size_t ml_part = 0, total = 0;
@@ -1692,6 +1694,7 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   const long long tile = 4096 / d->head_dim;
   const long long tiles = (static_cast<long long>(d->table_pages) * d->page_tokens + tile - 1) / tile;
   const int ctas = sambay::kv4::attn_ctas(d->head_dim, pl.nt, d->io == SAMBAY_F32);
+  if (pairs > 0x7FFFFFFFLL / tiles) return pl;          // grid 0: the line of tiles is too long
   pl.grid = static_cast<int>(std::min(static_cast<long long>(kSplitTarget) * ctas, pairs * tiles));
   pl.one_tile = tiles == 1;
   pl.many = pl.grid * static_cast<long long>(sambay::kv4::kWarps) > 8 * pairs;
@@ -1709,7 +1712,7 @@ sambay_status kv4_attn_launch(int dev, const sambay::kv4::AttnParams& p, const K
   auto kern = kv4_attn_kernel<T, D, NT, sizeof(T) == 4>;
   static bool attr_set[kMaxDevices] = {};
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) != cudaSuccess ||
         cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess)
       return SAMBAY_ERR_CUDA;
@@ -1717,7 +1720,7 @@ sambay_status kv4_attn_launch(int dev, const sambay::kv4::AttnParams& p, const K
   }
   {
     ProfScope ps("kv4_attn", st);
-    if (launch_k(kern, dim3(pl.grid), dim3(kThreads), kSmemBytes, st, false, 1, p) != cudaSuccess) return SAMBAY_ERR_CUDA;
+    if (launch_k(kern, dim3(pl.grid), dim3(kThreads), kAttnSmem, st, false, 1, p) != cudaSuccess) return SAMBAY_ERR_CUDA;
   }
   if (!pl.one_tile) {
     const long long rows = static_cast<long long>(p.pg.B) * p.T_ * p.Hq;
@@ -1741,7 +1744,7 @@ sambay_status kv4_attn_check(const sambay_kv4_dims* d, int32_t q_heads, int32_t 
   if (q_heads < 1 || tokens < 1) return SAMBAY_ERR_INVALID_ARG;
   if (q_heads % d->kv_heads != 0 || q_heads / d->kv_heads > 16 || tokens > kKv4MaxTokens)
     return SAMBAY_ERR_UNSUPPORTED;
-  return SAMBAY_OK;
+  return kv4_plan(d, q_heads, tokens).grid > 0 ? SAMBAY_OK : SAMBAY_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -1827,6 +1830,10 @@ sambay_status sambay_cross_attn_decode_kv4(const sambay_kv4_cache* c, const samb
   p.row_tiles = pl.row_tiles;
   p.cols = pl.cols;
   p.warps = pl.grid * sambay::kv4::kWarps;
+  p.page_bytes = d->kv_heads * (d->page_tokens / 16) * 18 * d->head_dim;
+  const int piece = std::min(d->page_tokens / 16, sambay::kv4::kStageTiles * 256 / d->head_dim);
+  p.piece_mask = (1u << piece) - 1;
+  p.piece_low = static_cast<uint32_t>(piece - 1);
   const float sc = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d->head_dim));
   p.scale_log2 = sc * sambay::kLog2e;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
