@@ -131,13 +131,41 @@ __device__ __forceinline__ uint32_t e4m3_code(float x) {              // nearest
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(x));
   return two & 0x7Fu;
 }
-// Bytes of two codes: e2m1(a) in the lower nibble, e2m1(b) in the upper one.
-__device__ __forceinline__ uint32_t e2m1_codes(float a, float b) {
-  uint32_t d;
-  asm("{\n\t.reg .b8 p, z;\n\tmov.b16 {p, z}, 0;\n\tcvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
-      "mov.b32 %0, {p, z, z, z};\n\t}"
-      : "=r"(d)
-      : "f"(a), "f"(b));
+// Eight codes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1_codes(float2 a, float2 b, float2 c, float2 d) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\t"
+      "mov.b32 %0, {p, q, r, s};\n\t}"
+      : "=r"(w)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+  return w;
+}
+
+// Pairs of f32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 
@@ -149,33 +177,44 @@ __device__ __forceinline__ uint32_t e2m1_codes(float a, float b) {
 // That decides rightly except where the exact quotient lies on a border
 // between two values (or, for f32, within the error of one).
 //   bf16: x and the border times the divisor have at most 8 significant bits,
-//     so a quotient that is not on a border is at least 2^-9 off it.  A factor
-//     of 1 + 2^-20 puts every quotient above its exact value, and cutting it to
-//     16 bits then gives a border exactly where it is one.
-//   f32: quotients within 2^-19 of a number of 4 bits (every border is one) are
-//     settled by comparing x with that number times the divisor, exact in f32.
+//     so a quotient that is not on a border is at least 2^-9 of it away.  Adding
+//     and taking away kRound leaves multiples of 2^-13 below 2^9: a quotient
+//     of e2m1 that is on a border becomes it (all are multiples of 1/4), the
+//     others stay on their side.  For the scale, a factor of 1 + 2^-20 puts
+//     every quotient above its exact value, and cutting it to 16 bits does the same.
+//   f32: the same rounding finds the quotients within 2^-14 of a number of 4
+//     bits (every border is one); comparing x with that number times the
+//     divisor, exact in f32, settles them.
+constexpr float kRound = 1536.0f;            // 1.5 x 2^10
+
+__device__ __forceinline__ float2 rounded(float2 x, float fac) {
+  return add2(fma2(x, make_float2(fac, fac), make_float2(kRound, kRound)), make_float2(-kRound, -kRound));
+}
+
 template <typename T> struct Four;
 template <> struct Four<bf16> {
   uint2 v;
   static constexpr uint32_t kInf = 0x7F80u;
   __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint2*>(p); }
   __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+  // two maxima side by side, until top_of()
   __device__ __forceinline__ uint32_t top() const {
-    const uint32_t m = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
-    return max(m & 0xFFFFu, m >> 16);
+    uint32_t m;
+    asm("{\n\t.reg .b32 a, b;\n\tabs.bf16x2 a, %1;\n\tabs.bf16x2 b, %2;\n\tmax.NaN.bf16x2 %0, a, b;\n\t}" : "=r"(m) : "r"(v.x), "r"(v.y));
+    return m;
   }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+  static __device__ __forceinline__ uint32_t top_of(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
   static __device__ __forceinline__ float top_value(uint32_t bits) { return __uint_as_float(bits << 16); }
-  static __device__ __forceinline__ float cut(float y) { return __uint_as_float(__float_as_uint(y) & 0xFFFFFF80u); }
   // e4m3 code of amax / 6 * two; two: a power of two
   static __device__ __forceinline__ uint32_t scale_code(float amax, float two) {
-    return e4m3_code(fminf(cut(amax * two * (0.16666667f * 1.00000095f)), 448.0f));
+    const float y = amax * two * (0.16666667f * 1.00000095f);
+    return e4m3_code(fminf(__uint_as_float(__float_as_uint(y) & 0xFFFFFF80u), 448.0f));
   }
-  // the factor of e2m1's argument
-  static __device__ __forceinline__ float factor(float s, float two) { return __fdividef(1.00000095f, s) * two; }
-  __device__ __forceinline__ uint32_t codes(float fac, float, float) const {
-    const uint32_t lo = e2m1_codes(cut(__uint_as_float(v.x << 16) * fac), cut(__uint_as_float(v.x & 0xFFFF0000u) * fac));
-    const uint32_t hi = e2m1_codes(cut(__uint_as_float(v.y << 16) * fac), cut(__uint_as_float(v.y & 0xFFFF0000u) * fac));
-    return lo | hi << 8;
+  // the four over the scale (fac: 2^-e over it), rounded as said
+  __device__ __forceinline__ void quotients(float fac, float, float, float2& a, float2& b) const {
+    a = rounded(make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u)), fac);
+    b = rounded(make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u)), fac);
   }
 };
 template <> struct Four<float> {
@@ -187,6 +226,8 @@ template <> struct Four<float> {
   __device__ __forceinline__ uint32_t top() const {
     return max(max(abs_bits(v.x), abs_bits(v.y)), max(abs_bits(v.z), abs_bits(v.w)));
   }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t top_of(uint32_t m) { return m; }
   static __device__ __forceinline__ float top_value(uint32_t bits) { return __uint_as_float(bits); }
   static __device__ __forceinline__ uint32_t scale_code(float amax, float two) {
     const float a = amax * two;
@@ -199,20 +240,18 @@ template <> struct Four<float> {
     if (a > up || (a == up && odd && c < 126)) return c + 1;
     return a < down || (a == down && odd) ? c - 1 : c;
   }
-  static __device__ __forceinline__ float factor(float s, float two) { return __fdividef(1.0f, s) * two; }
-  // x over s * 2^e, on the right side of a border that it is near (s2: s * 2^e)
-  static __device__ __forceinline__ float quotient(float x, float fac, float s, float two) {
-    const float y = x * fac;
-    const uint32_t yb = __float_as_uint(y);
-    if (((yb + 16u) & 0xFFFFFu) >= 32u) return y;
-    const uint32_t cb = (yb + 16u) & ~0xFFFFFu;
-    const float ax = fabsf(x * two), t = fabsf(__uint_as_float(cb)) * s;
-    return __uint_as_float(ax > t ? cb + 1u : ax < t && (cb & 0x7FFFFFFFu) ? cb - 1u : cb);
+  // x over s * 2^e, on the right side of a border that it is near
+  static __device__ __forceinline__ float settled(float x, float y, float s, float two) {
+    const uint32_t b = __float_as_uint(y);
+    if ((b & 0xFFFFFu) != 0 || y == 0.0f) return y;
+    const float ax = fabsf(x * two), t = fabsf(y) * s;
+    return __uint_as_float(ax > t ? b + 1u : ax < t ? b - 1u : b);
   }
-  __device__ __forceinline__ uint32_t codes(float fac, float s, float two) const {
-    const uint32_t lo = e2m1_codes(quotient(v.x, fac, s, two), quotient(v.y, fac, s, two));
-    const uint32_t hi = e2m1_codes(quotient(v.z, fac, s, two), quotient(v.w, fac, s, two));
-    return lo | hi << 8;
+  __device__ __forceinline__ void quotients(float fac, float s, float two, float2& a, float2& b) const {
+    a = rounded(make_float2(v.x, v.y), fac);
+    b = rounded(make_float2(v.z, v.w), fac);
+    a = make_float2(settled(v.x, a.x, s, two), settled(v.y, a.y, s, two));
+    b = make_float2(settled(v.z, b.x, s, two), settled(v.w, b.y, s, two));
   }
 };
 
@@ -226,6 +265,8 @@ __device__ __forceinline__ void store4(bf16* p, float2 a, float2 b) {
   *reinterpret_cast<uint2*>(p) = make_uint2(u.u.x, u.u.y);
 }
 
+constexpr int kRowWarps = 4;     // of a CTA (4 x 32768 bf16 tokens written: 151 us, with 8 warps 156 us)
+
 template <typename T>
 struct RowParams {
   Pages pg;
@@ -236,6 +277,8 @@ struct RowParams {
   const int32_t* pos;      // [B] cached tokens before the call's
   const int32_t* count;    // [B] rows of each sequence, or null (T)
   int T_, groups;          // groups: of 16 tokens that T rows may touch, (T + 30) / 16
+  int heads_log2;          // of a CTA's warps, 2^heads_log2 side by side over the row, the others over the groups
+  unsigned head_ctas;      // CTAs over a row
   long long k_stride, v_stride;
 };
 
@@ -259,35 +302,38 @@ struct Unit {
   uint8_t* grp;            // null: nothing to do
 
   template <typename T>
-  __device__ __forceinline__ Unit(const RowParams<T>& p, long long u) {
+  __device__ __forceinline__ explicit Unit(const RowParams<T>& p) {
     constexpr int C = D / 64;
-    const int heads = p.pg.Hkv * C;
-    const int hc = static_cast<int>(u % heads);
-    const long long k = u / heads;
-    b = static_cast<int>(k / p.groups);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // CTAs over the row first: those that run together work on whole rows
+    const unsigned deep = blockIdx.x / p.head_ctas, along = blockIdx.x - deep * p.head_ctas;
+    const int hc = (along << p.heads_log2) + (warp & ((1 << p.heads_log2) - 1));
+    const int gi = deep * (kRowWarps >> p.heads_log2) + (warp >> p.heads_log2);
+    b = blockIdx.y;
     col = hc * 64;
     c = hc % C;
-    const int lane = threadIdx.x & 31;
-    const int n = rows_of(p.count, b, p.T_, hc == 0 && k % p.groups == 0);
-    const int pos = p.pos[b];
-    // the group's first position, and the call's rows in it
-    const long long at = ((static_cast<long long>(pos) >> 4) + k % p.groups) * kGroup;
     grp = nullptr;
     row[0] = row[1] = -1;
     all = false;
-    if (n == 0 || at >= static_cast<long long>(pos) + n) return;
-    const int at32 = static_cast<int>(min(max(at, -1LL), 0x7FFFFFFFLL));      // what is cut is outside any table
-    grp = group_of<D>(p.pg, b, hc / C, at32);
+    if (hc >= p.pg.Hkv * C || gi >= p.groups) return;
+    const int n = rows_of(p.count, b, p.T_, hc == 0 && gi == 0);
+    const int pos = p.pos[b];
+    // the group's place in the sequence, and its first token's row of the call (from -15 on)
+    const int at16 = (pos >> 4) + gi;
+    const long long r0 = static_cast<long long>(at16) * kGroup - pos;
+    if (n == 0 || r0 >= n) return;
+    // what no table reaches stays outside it
+    grp = group_of<D>(p.pg, b, hc / C, at16 < 0 ? -1 : min(at16, 1 << 26) * kGroup);
     if (!grp) {
       if (lane == 0) record_status(kStatusBadIndex);
       return;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const long long r = at + (lane >> 2) + 8 * i - pos;
+      const long long r = r0 + (lane >> 2) + 8 * i;
       row[i] = r >= 0 && r < n ? static_cast<int>(r) : -1;
     }
-    all = at >= pos && at + kGroup <= static_cast<long long>(pos) + n;
+    all = r0 >= 0 && r0 + kGroup <= n;
   }
 };
 
@@ -301,11 +347,12 @@ __device__ __forceinline__ void quantise(const Four<T> (&x)[2][4], float two, ui
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const uint32_t m0 = x[0][b].top(), m1 = x[1][b].top();
-    m[b] = max(t & 1 ? m1 : m0, __shfl_xor_sync(0xFFFFFFFFu, t & 1 ? m0 : m1, 1));
+    m[b] = Four<T>::most(t & 1 ? m1 : m0, __shfl_xor_sync(0xFFFFFFFFu, t & 1 ? m0 : m1, 1));
   }
 #pragma unroll
   for (int b = 0; b < 2; ++b)
-    w[b] = max(t & 2 ? m[2 + b] : m[b], __shfl_xor_sync(0xFFFFFFFFu, t & 2 ? m[b] : m[2 + b], 2));
+    w[b] = Four<T>::top_of(
+        Four<T>::most(t & 2 ? m[2 + b] : m[b], __shfl_xor_sync(0xFFFFFFFFu, t & 2 ? m[b] : m[2 + b], 2)));
   uint32_t code = 0;
   float s[2], fac[2];
 #pragma unroll
@@ -313,22 +360,22 @@ __device__ __forceinline__ void quantise(const Four<T> (&x)[2][4], float two, ui
     const bool bad = w[b] >= Four<T>::kInf;
     const uint32_t c = bad ? 0x7Fu : Four<T>::scale_code(Four<T>::top_value(w[b]), two);
     s[b] = bad ? 0.0f : e4m3_value(c);
-    fac[b] = s[b] > 0.0f ? Four<T>::factor(s[b], two) : 0.0f;      // 0: codes of 0
+    fac[b] = s[b] > 0.0f ? __fdividef(two, s[b]) : 0.0f;           // 0: codes of 0
     code |= c << (8 * b);
   }
   scales = code | __shfl_xor_sync(0xFFFFFFFFu, code, 2) << 16;     // as it should be in lanes t = 0, 1
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t c16[4];
+    float2 y[8];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const int src = (lane & ~3) | i | (b >> 1) << 1;
       const float f = __shfl_sync(0xFFFFFFFFu, fac[b & 1], src);
       const float sb = sizeof(T) == 4 ? __shfl_sync(0xFFFFFFFFu, s[b & 1], src) : 0.0f;
-      c16[b] = x[i][b].codes(f, sb, two);
+      x[i][b].quotients(f, sb, two, y[2 * b], y[2 * b + 1]);
     }
-    codes[i][0] = c16[0] | c16[1] << 16;
-    codes[i][1] = c16[2] | c16[3] << 16;
+    codes[i][0] = e2m1_codes(y[0], y[1], y[2], y[3]);
+    codes[i][1] = e2m1_codes(y[4], y[5], y[6], y[7]);
   }
 }
 
@@ -371,11 +418,9 @@ __device__ __forceinline__ void load_rows(const T* p, long long stride, const in
 // values: K's codes and both scales are stored per token; of V's codes, where
 // two tokens share a byte, a group that is not all the call's is read first.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv4_write_kernel(const RowParams<T> p) {
+__global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 4 : 10) kv4_write_kernel(const RowParams<T> p) {
   const Pages& pg = p.pg;
-  const long long u = (blockIdx.x * 256LL + threadIdx.x) >> 5;
-  if (u >= static_cast<long long>(pg.B) * p.groups * pg.Hkv * (D / 64)) return;
-  const Unit<D> un(p, u);
+  const Unit<D> un(p);
   if (!un.grp) return;                 // the whole warp's
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   constexpr int KS = D / 16;
@@ -450,11 +495,9 @@ __device__ __forceinline__ void store_rows(T* p, long long stride, const int (&r
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv4_read_kernel(const RowParams<T> p) {
+__global__ void __launch_bounds__(32 * kRowWarps) kv4_read_kernel(const RowParams<T> p) {
   const Pages& pg = p.pg;
-  const long long u = (blockIdx.x * 256LL + threadIdx.x) >> 5;
-  if (u >= static_cast<long long>(pg.B) * p.groups * pg.Hkv * (D / 64)) return;
-  const Unit<D> un(p, u);
+  const Unit<D> un(p);
   if (!un.grp) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   constexpr int KS = D / 16;
@@ -552,32 +595,6 @@ __device__ __forceinline__ void mma16816_f16_zero(float (&d)[4], uint32_t a0, ui
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-// Pairs of f32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // A warp's ring: bulk copies that complete on one mbarrier a stage.
 __device__ __forceinline__ void bar_init(uint32_t bar) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");

@@ -1638,16 +1638,24 @@ sambay::kv4::Pages kv4_pages(const sambay_kv4_cache* c, const sambay_kv4_dims* d
 sambay_status kv4_check_rows(const sambay_kv4_dims* d, int32_t tokens) {
   if (tokens < 1) return SAMBAY_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(d->batch) * tokens;
-  if (rows > (1LL << 33) / d->kv_heads) return SAMBAY_ERR_UNSUPPORTED;   // CTAs within a grid's 2^31
+  if (rows > (1LL << 36) / d->kv_heads) return SAMBAY_ERR_UNSUPPORTED;
+  // a grid's CTAs along x: at most one for each 16 tokens and 64 values of a row
+  if ((tokens / 16 + 2LL) * d->kv_heads * (d->head_dim / 64) > 0x7FFFFFFFLL) return SAMBAY_ERR_UNSUPPORTED;
   return SAMBAY_OK;
 }
 
 template <typename T, int D>
-sambay_status kv4_rows_launch(bool write, const sambay::kv4::RowParams<T>& p, cudaStream_t st) {
-  const long long units = static_cast<long long>(p.pg.B) * p.groups * p.pg.Hkv * (D / 64);
-  auto kern = write ? sambay::kv4::kv4_write_kernel<T, D> : sambay::kv4::kv4_read_kernel<T, D>;
+sambay_status kv4_rows_launch(bool write, sambay::kv4::RowParams<T>& p, cudaStream_t st) {
+  using namespace sambay::kv4;
+  const int parts = p.pg.Hkv * (D / 64);            // of 64 values, a warp each
+  // as many side by side as leave no warp without one
+  while ((2 << p.heads_log2) <= kRowWarps && !(parts >> p.heads_log2 & 1)) ++p.heads_log2;
+  const int wide = 1 << p.heads_log2, deep = kRowWarps / wide;
+  p.head_ctas = static_cast<unsigned>(parts / wide);
+  auto kern = write ? kv4_write_kernel<T, D> : kv4_read_kernel<T, D>;
   ProfScope ps(write ? "kv4_write" : "kv4_read", st);
-  return launch_k(kern, dim3(static_cast<unsigned>((units + 7) / 8)), dim3(256), 0, st, false, 1, p) == cudaSuccess
+  return launch_k(kern, dim3(p.head_ctas * static_cast<unsigned>((p.groups + deep - 1) / deep), p.pg.B), dim3(32 * kRowWarps), 0, st,
+                  false, 1, p) == cudaSuccess
              ? SAMBAY_OK
              : SAMBAY_ERR_CUDA;
 }
