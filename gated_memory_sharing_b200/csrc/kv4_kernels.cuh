@@ -64,8 +64,14 @@ struct Pages {
   int B, Hkv, page_log2, num_pages, table_pages;   // P = 2^page_log2 tokens
 };
 
+// One of the small index arrays' values.  EARLY: by a kernel that has not yet
+// waited for the one in front of it; through L2, past what an SM may have kept.
+template <bool EARLY>
+__device__ __forceinline__ int index_at(const int32_t* p, int i) { return EARLY ? __ldcg(p + i) : p[i]; }
+
+template <bool EARLY = false>
 __device__ __forceinline__ int head_exp(const int32_t* e, int h) {
-  return e ? max(-kMaxExp, min(kMaxExp, e[h])) : 0;
+  return e ? max(-kMaxExp, min(kMaxExp, index_at<EARLY>(e, h))) : 0;
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
@@ -211,6 +217,16 @@ template <> struct Four<bf16> {
     const float y = amax * two * (0.16666667f * 1.00000095f);
     return e4m3_code(fminf(__uint_as_float(__float_as_uint(y) & 0xFFFFFF80u), 448.0f));
   }
+  __device__ __forceinline__ void values(float (&x)[4]) const {
+    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
+  // the largest |x| that is a number
+  __device__ __forceinline__ float top_abs() const {
+    float x[4];
+    values(x);
+    return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+  }
   // the four over the scale (fac: 2^-e over it), rounded as said
   __device__ __forceinline__ void quotients(float fac, float, float, float2& a, float2& b) const {
     a = rounded(make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u)), fac);
@@ -239,6 +255,10 @@ template <> struct Four<float> {
     const bool odd = c & 1u;
     if (a > up || (a == up && odd && c < 126)) return c + 1;
     return a < down || (a == down && odd) ? c - 1 : c;
+  }
+  __device__ __forceinline__ void values(float (&x)[4]) const { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
+  __device__ __forceinline__ float top_abs() const {
+    return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
   }
   // x over s * 2^e, on the right side of a border that it is near
   static __device__ __forceinline__ float settled(float x, float y, float s, float two) {
@@ -283,9 +303,10 @@ struct RowParams {
 };
 
 // Rows of sequence b: min(count, T) of them; a count outside 0 .. T is recorded.
+template <bool EARLY = false>
 __device__ __forceinline__ int rows_of(const int32_t* count, int b, int T, bool tell) {
   if (!count) return T;
-  const int n = count[b];
+  const int n = index_at<EARLY>(count, b);
   if ((n < 0 || n > T) && tell) record_status(kStatusBadIndex);
   return max(0, min(T, n));
 }
@@ -420,6 +441,7 @@ __device__ __forceinline__ void load_rows(const T* p, long long stride, const in
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 4 : 10) kv4_write_kernel(const RowParams<T> p) {
   const Pages& pg = p.pg;
+  pdl_wait();
   const Unit<D> un(p);
   if (!un.grp) return;                 // the whole warp's
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -497,6 +519,7 @@ __device__ __forceinline__ void store_rows(T* p, long long stride, const int (&r
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kRowWarps) kv4_read_kernel(const RowParams<T> p) {
   const Pages& pg = p.pg;
+  pdl_wait();
   const Unit<D> un(p);
   if (!un.grp) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -552,6 +575,7 @@ struct AttnParams {
   float* o_part;           // [warp][first or last pair][cols, D]  partial outputs
   float* ml_part;          // [warp][first or last pair][cols, 2]  their (largest logit, in base 2 and less kPShift; l)
   int T_, Hq, G;
+  int group_inv;           // ceil(2^16 / G): r * group_inv >> 16 is r / G (r < 256, G <= 16)
   int row_tiles, cols;     // cols: min(8 NT, G T) columns of a row tile
   int page_bytes;
   uint32_t piece_mask, piece_low;      // groups of a page that a stage may hold: a bit each; their number less 1
@@ -625,8 +649,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // Cached tokens of sequence b, inside the table; `tell` records a length outside it.
+template <bool EARLY = false>
 __device__ __forceinline__ int len_of(const AttnParams& p, int b, bool tell) {
-  const int len = p.lens[b], cap = p.pg.table_pages << p.pg.page_log2;
+  const int len = index_at<EARLY>(p.lens, b), cap = p.pg.table_pages << p.pg.page_log2;
   if (tell && (len < 0 || len > cap)) record_status(kStatusBadIndex);
   return max(0, min(cap, len));
 }
@@ -647,24 +672,27 @@ struct Line {
   }
 };
 
-// The line of a call, and the tile in it at which sequence b begins (one warp).
+__device__ __forceinline__ Line make_line(const AttnParams& p, int tiles) {
+  Line line;
+  line.shares = min(tiles, p.warps);
+  line.base = static_cast<unsigned>(tiles) / static_cast<unsigned>(line.shares);
+  line.rem = tiles - line.base * line.shares;
+  return line;
+}
+
+// The line of a call, and the tile in it at which sequence b begins (one warp of
+// the combine kernel).
 template <int D>
-__device__ __forceinline__ Line line_of(const AttnParams& p, int b, bool tell, int* before) {
+__device__ __forceinline__ Line line_of(const AttnParams& p, int b, int* before) {
   int s = 0, sb = 0;
   for (int i = threadIdx.x & 31; i < p.pg.B; i += 32) {
-    const int n = tiles_of<D>(len_of(p, i, tell));
+    const int n = tiles_of<D>(len_of<true>(p, i, false));
     s += n;
     if (i < b) sb += n;
   }
-  s = __reduce_add_sync(0xFFFFFFFFu, s);
-  sb = __reduce_add_sync(0xFFFFFFFFu, sb);
   const int pairs = p.pg.Hkv * p.row_tiles;
-  *before = sb * pairs;
-  Line line;
-  line.shares = min(s * pairs, p.warps);
-  line.base = s * pairs / line.shares;
-  line.rem = s * pairs - line.base * line.shares;
-  return line;
+  *before = __reduce_add_sync(0xFFFFFFFFu, sb) * pairs;
+  return make_line(p, __reduce_add_sync(0xFFFFFFFFu, s) * pairs);
 }
 
 // A place in the line.
@@ -691,37 +719,60 @@ __device__ __forceinline__ bool advance(const AttnParams& p, Cursor& c, int n) {
   return true;
 }
 
-// Tile x of the line.
-template <int D>
-__device__ __forceinline__ Cursor find(const AttnParams& p, int x) {
+// Inclusive sums over the warp's lanes.
+__device__ __forceinline__ int scan(int v) {
   const int lane = threadIdx.x & 31;
-  const int pairs = p.pg.Hkv * p.row_tiles;
-  Cursor c{};
-  for (int b0 = 0; b0 < p.pg.B; b0 += 32) {
-    const int len = b0 + lane < p.pg.B ? len_of(p, b0 + lane, false) : 0;
-    const int n = b0 + lane < p.pg.B ? tiles_of<D>(len) : 0;
-    int upto = n * pairs;                                          // of this and the sequences before it
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const unsigned past = __ballot_sync(0xFFFFFFFFu, upto > x);
-    if (past) {
-      const int k = __ffs(past) - 1;
-      c.b = b0 + k;
-      c.len = __shfl_sync(0xFFFFFFFFu, len, k);
-      c.tiles = __shfl_sync(0xFFFFFFFFu, n, k);
-      const int in = x - (__shfl_sync(0xFFFFFFFFu, upto, k) - c.tiles * pairs);
-      const int pair = in / c.tiles;
-      c.tile = in - pair * c.tiles;
-      c.h = pair / p.row_tiles;
-      c.rt = pair - c.h * p.row_tiles;
-      return c;
-    }
-    x -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
   }
-  return c;                                                        // not reached: x is in the line
+  return v;
+}
+
+// The line, and the place in it where share gw begins (one warp; the place of
+// a share that is none is not set).  A lane sums the tiles of B / 32 sequences;
+// then the sequences of the lane that holds the place are looked through.
+template <int D>
+__device__ __forceinline__ Line begin_of(const AttnParams& p, int gw, Cursor& c, int* begin) {
+  const int lane = threadIdx.x & 31;
+  const int pairs = p.pg.Hkv * p.row_tiles, per = (p.pg.B + 31) >> 5;
+  int mine = 0, len = 0;
+  for (int i = lane * per; i < min(p.pg.B, lane * per + per); ++i) {
+    len = len_of(p, i, gw == 0);
+    mine += tiles_of<D>(len);
+  }
+  const int upto = scan(mine);                       // tiles of one pair of these sequences and those before
+  const Line line = make_line(p, __shfl_sync(0xFFFFFFFFu, upto, 31) * pairs);
+  if (gw >= line.shares) return line;
+  *begin = line.begin(gw);
+  int x = *begin;
+  int k = __ffs(__ballot_sync(0xFFFFFFFFu, upto * pairs > x)) - 1;
+  x -= __shfl_sync(0xFFFFFFFFu, upto - mine, k) * pairs;
+  c.b = k;
+  if (per > 1) {
+    for (int b0 = k * per;; b0 += 32) {              // ends: x is in the line
+      const int i = b0 + lane;
+      len = i < p.pg.B ? len_of(p, i, false) : 0;
+      mine = i < p.pg.B ? tiles_of<D>(len) : 0;
+      const int sum = scan(mine);
+      const unsigned past = __ballot_sync(0xFFFFFFFFu, sum * pairs > x);
+      if (past) {
+        k = __ffs(past) - 1;
+        x -= __shfl_sync(0xFFFFFFFFu, sum - mine, k) * pairs;
+        c.b = b0 + k;
+        break;
+      }
+      x -= __shfl_sync(0xFFFFFFFFu, sum, 31) * pairs;
+    }
+  }
+  c.len = __shfl_sync(0xFFFFFFFFu, len, k);
+  c.tiles = tiles_of<D>(c.len);
+  const int pair = static_cast<unsigned>(x) / static_cast<unsigned>(c.tiles);
+  c.tile = x - pair * c.tiles;
+  c.h = p.row_tiles == 1 ? pair : pair / p.row_tiles;
+  c.rt = pair - c.h * p.row_tiles;
+  return line;
 }
 
 // Query row r of a (sequence, KV head): token r / G, head r % G of the group.
@@ -737,7 +788,6 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   constexpr int SG = kStageTiles * GP;                                  // groups of a stage
   constexpr int S = kStages, kStageBytes = kStageTiles * kTileBytes;
   extern __shared__ __align__(128) uint8_t smem[];
-  pdl_launch_dependents();             // the combine kernel's CTAs come as this one's leave
   const Pages& pg = p.pg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -747,15 +797,17 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   const uint32_t ring_addr = shared_addr(ring);
   const uint32_t bars = shared_addr(smem + kWarps * S * kStageBytes) + warp * (S * 8);
 
-  int none;
-  const Line line = line_of<D>(p, 0, gw == 0, &none);
+  pdl_wait();
+  pdl_launch_dependents();             // the combine kernel's CTAs come as this one's leave
+  Cursor c{};                          // the tile being worked on
+  int begin = 0;
+  const Line line = begin_of<D>(p, gw, c, &begin);
   if (gw >= line.shares) return;
-  const int begin = line.begin(gw), share = line.begin(gw + 1) - begin;
+  const int share = line.begin(gw + 1) - begin;
   if (lane < S) bar_init(bars + 8 * lane);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
 
-  Cursor c = find<D>(p, begin);        // the tile being worked on
   Cursor in = c;                       // the next tile to load
 
   // Pages of the 32 groups of the loading cursor's window, one a lane.
@@ -797,6 +849,27 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
     loaded += n;
     window = advance<D>(p, in, n);
   };
+  // The queries of a pair, as they lie there: column g's values 16 b + 4 t .. + 3.
+  Four<T> raw[NT][KS];
+  int nq = 0, kexp = 0;                // query tokens of the sequence; the head's exponent
+  auto fetch = [&]() {
+    const int row0 = c.rt * (8 * NT);
+    nq = rows_of(p.count, c.b, p.T_, c.h == 0 && row0 == 0);
+    kexp = head_exp(pg.k_exp, c.h);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = row0 + 8 * n + g, tok = r * p.group_inv >> 16;
+      const T* qr = static_cast<const T*>(p.q) +
+                    ((static_cast<long long>(c.b) * p.T_ + tok) * p.Hq + c.h * p.G + r - tok * p.G) * D + 4 * t;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        if (r < nq * p.G)
+          raw[n][ks].load(qr + 16 * ks);
+        else
+          raw[n][ks].zero();
+    }
+  };
+  fetch();                             // on their way while the first pages are looked up
   issue(0);
 
   uint32_t qb[NQ][NT][KS][2];
@@ -812,29 +885,15 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
     if (loaded < share) issue(st ^ 1);
     if (fresh) {
       // B fragments of Q (column g of n-tile n), and per accumulator column its factor and its last token
+      if (i > 0) fetch();
       fresh = false;
-      const int h = c.h, row0 = c.rt * (8 * NT);
-      const int nq = rows_of(p.count, c.b, p.T_, h == 0 && row0 == 0);
       lim_min = c.len;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int r = row0 + 8 * n + g;
-        const bool real = r < nq * p.G;
-        const int tok = r / p.G;
-        float x[KS][4];
+        const int r = c.rt * (8 * NT) + 8 * n + g;
         float am = 0.0f;
-        const T* qr =
-            static_cast<const T*>(p.q) + ((static_cast<long long>(c.b) * p.T_ + tok) * p.Hq + h * p.G + r % p.G) * D;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          x[ks][0] = x[ks][1] = x[ks][2] = x[ks][3] = 0.0f;
-          if (real) {
-            load2(qr + 16 * ks + 4 * t, x[ks]);
-            load2(qr + 16 * ks + 4 * t + 2, x[ks] + 2);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) am = fmaxf(am, fabsf(x[ks][e]));
-        }
+        for (int ks = 0; ks < KS; ++ks) am = fmaxf(am, raw[n][ks].top_abs());
         am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
         am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
         // the row's largest value to 2^14 .. 2^15; zeros, infinities as they are
@@ -843,22 +902,26 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
         const int exa = max(-100, min(100, -ex));
         const float down0 = pow2i(exa), down1 = pow2i(-ex - exa);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks) {
+          float x[4];
+          raw[n][ks].values(x);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float u = x[ks][2 * e] * down0 * down1, v = x[ks][2 * e + 1] * down0 * down1;
+            const float u = x[2 * e] * down0 * down1, v = x[2 * e + 1] * down0 * down1;
             qb[0][n][ks][e] = pack_f16(u, v);
             if (SPLIT) {
               const float2 hi = f16x2_f32(qb[0][n][ks][e]);
               qb[NQ - 1][n][ks][e] = pack_f16(u - hi.x, v - hi.y);
             }
           }
+        }
         // scale * log2(e) * 2^(row + head), in two steps so that each stays finite
-        const int e2 = ex + head_exp(pg.k_exp, h);                     // -204 .. 177
+        const int e2 = ex + kexp;                                      // -204 .. 177
         const int e2a = max(-100, min(100, e2));
         // kept normal and finite: a masked -infinity times it stays one
         const float fac = fminf(fmaxf(p.scale_log2 * pow2i(e2a) * pow2i(e2 - e2a), 1.2e-38f), 3e38f);
-        const int limit = real ? c.len - (nq - 1 - tok) : 0x7FFFFFFF;  // columns that are none see all, and are not written
+        // columns that are none see all, and are not written
+        const int limit = r < nq * p.G ? c.len - (nq - 1 - (r * p.group_inv >> 16)) : 0x7FFFFFFF;
         lim_min = min(lim_min, limit);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -1068,7 +1131,6 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
     if (c.tile + n == c.tiles || i + n == share) {
       // the pair, or this warp's share of it, is done
       const int h = c.h, row0 = c.rt * (8 * NT);
-      const int nq = rows_of(p.count, c.b, p.T_, false);
       const float ve = pow2i(head_exp(pg.v_exp, h));
       const bool from_start = i >= c.tile;                     // the pair's first tile is in this share
       const bool done = from_start && c.tile + n == c.tiles;
@@ -1086,8 +1148,9 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
           if (r < nq * p.G) {
             if (done) {
               const float inv = ls == 0.0f ? 0.0f : ve / ls;
+              const int tok = r * p.group_inv >> 16;
               T* dst = static_cast<T*>(p.out) +
-                       ((static_cast<long long>(c.b) * p.T_ + r / p.G) * p.Hq + h * p.G + r % p.G) * D;
+                       ((static_cast<long long>(c.b) * p.T_ + tok) * p.Hq + h * p.G + r - tok * p.G) * D;
 #pragma unroll
               for (int k = 0; k < KS; ++k) store2(dst + 16 * k + 2 * g, o[n][k][e] * inv, o[n][k][e + 2] * inv);
             } else {
@@ -1105,76 +1168,90 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   }
 }
 
+// A running sum of parts of one row: values relative to 2^m, and what they are to be divided by.
+template <int V>
+struct RowSum {
+  float m = -kNoRef, den = 0.0f, num[V] = {};
+  __device__ __forceinline__ void add(float m2, float den2, const float (&x)[V]) {
+    const float to = fmaxf(m, m2), f = ex2_approx(m - to), f2 = ex2_approx(m2 - to);
+    m = to;
+    den = den * f + den2 * f2;
+#pragma unroll
+    for (int v = 0; v < V; ++v) num[v] = num[v] * f + x[v] * f2;
+  }
+};
+
 // Rows whose pair was shared by several warps, from their parts in the line's
-// order.  WARPS warps a row (8 where a pair has many parts, else 1).
-template <typename T, int D, int NT, int WARPS>
+// order.  Grid (rows of a sequence or slices of them, sequences).
+//   MANY = false: a warp a row, D / 32 values a lane.
+//   MANY: a CTA for 32 values of a row; 8 lanes take 4 values each, 32 of them
+//   every 32nd part, and then their sums are added in order.
+template <typename T, int D, int NT, bool MANY>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
-  constexpr int V = D / 32;            // values a lane
+  constexpr int V = MANY ? 4 : D / 32, SLICES = MANY ? D / 32 : 1;
   const Pages& pg = p.pg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = WARPS == 1 ? blockIdx.x * 8LL + warp : blockIdx.x;
-  const bool in = row < static_cast<long long>(pg.B) * p.T_ * p.Hq;
-  const int hq = in ? static_cast<int>(row % p.Hq) : 0;
-  const int tok = in ? static_cast<int>(row / p.Hq % p.T_) : 0, b = in ? static_cast<int>(row / p.Hq / p.T_) : 0;
-  const bool live = in && tok < rows_of(p.count, b, p.T_, false);
-  const int h = hq / p.G, r = tok * p.G + hq % p.G;
+  const int row = MANY ? blockIdx.x / SLICES : blockIdx.x * 8 + warp, b = blockIdx.y;
+  const int tok = row / p.Hq, hq = row - tok * p.Hq;
+  const int h = hq / p.G, r = tok * p.G + hq - h * p.G;
   const int pair = h * p.row_tiles + r / (8 * NT), col = r % (8 * NT);
+  const int at = MANY ? blockIdx.x % SLICES * 32 + (threadIdx.x & 7) * 4 : lane * V;       // first of the lane's values
   int before;
-  const Line line = line_of<D>(p, b, false, &before);
-  const int tiles = tiles_of<D>(len_of(p, b, false));
+  const Line line = line_of<D>(p, b, &before);
+  const int tiles = tiles_of<D>(len_of<true>(p, b, false));
   const int a = before + pair * tiles;
   const int w0 = line.share_of(a), w1 = line.share_of(a + tiles - 1);
   const int first = line.begin(w0) == a ? 0 : 1;
+  const bool live = tok < rows_of<true>(p.count, b, p.T_, false);
+  const float ve = pow2i(head_exp<true>(pg.v_exp, min(h, pg.Hkv - 1)));
   // what was read so far no kernel of this call writes; every thread waits, so
   // that this kernel does not end before the one whose parts it reads
   pdl_wait();
-  if (!live || w0 == w1) return;       // w0 == w1: finished by that warp
-  auto slot = [&](int w) { return (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col; };
-  float ms = -kNoRef;
-  for (int w = w0 + lane; w <= w1; w += 32) ms = fmaxf(ms, p.ml_part[slot(w) * 2]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xFFFFFFFFu, ms, o));
-  float num[V], den = 0.0f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) num[v] = 0.0f;
-  // this warp's run of the parts
-  const int n = w1 - w0 + 1, per = (n + WARPS - 1) / WARPS;
-  const int lo = w0 + (WARPS == 1 ? 0 : warp * per), hi = min(w1 + 1, lo + per);
+  pdl_launch_dependents();
+  if (!live || w0 == w1) return;       // the whole CTA's where MANY; w0 == w1: finished by that warp
+  RowSum<V> sum;
+  const int step = MANY ? 32 : 1;
 #pragma unroll 4
-  for (int w = lo; w < hi; ++w) {
-    const long long k = slot(w);
+  for (int w = w0 + (MANY ? threadIdx.x >> 3 : 0); w <= w1; w += step) {
+    const long long k = (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col;
     const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + k * 2);
-    const float fw = ex2_approx(ml.x - ms);
+    float x[V];
 #pragma unroll
-    for (int v = 0; v < V; v += 2) {
-      float x[2];
-      load2(p.o_part + k * D + lane * V + v, x);
-      num[v] = fmaf(fw, x[0], num[v]);
-      num[v + 1] = fmaf(fw, x[1], num[v + 1]);
-    }
-    den = fmaf(fw, ml.y, den);
+    for (int v = 0; v < V; v += 2) load2(p.o_part + k * D + at + v, x + v);
+    sum.add(ml.x, ml.y, x);
   }
-  if (WARPS > 1) {
-    __shared__ float sh[WARPS][D + 1];
+  if (MANY) {
+    // the four of a warp, then the warps
 #pragma unroll
-    for (int v = 0; v < V; ++v) sh[warp][lane * V + v] = num[v];
-    if (lane == 0) sh[warp][D] = den;
+    for (int o = 8; o < 32; o <<= 1) {
+      float x[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = __shfl_xor_sync(0xFFFFFFFFu, sum.num[v], o);
+      sum.add(__shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.den, o), x);
+    }
+    __shared__ float sh[8][8][V + 2];
+    if (lane < 8) {
+      float* mine = sh[warp][lane];
+      mine[V] = sum.m;
+      mine[V + 1] = sum.den;
+#pragma unroll
+      for (int v = 0; v < V; ++v) mine[v] = sum.num[v];
+    }
     __syncthreads();
-    if (warp != 0) return;
-    den = 0.0f;
+    if (threadIdx.x >= 8) return;
 #pragma unroll
-    for (int v = 0; v < V; ++v) num[v] = 0.0f;
+    for (int k = 1; k < 8; ++k) {
+      const float* other = sh[k][lane];
+      float x[V];
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) num[v] += sh[w][lane * V + v];
-      den += sh[w][D];
+      for (int v = 0; v < V; ++v) x[v] = other[v];
+      sum.add(other[V], other[V + 1], x);
     }
   }
-  const float inv = den == 0.0f ? 0.0f : pow2i(head_exp(pg.v_exp, h)) / den;
-  T* dst = static_cast<T*>(p.out) + row * D + lane * V;
+  const float inv = sum.den == 0.0f ? 0.0f : ve / sum.den;
+  T* dst = static_cast<T*>(p.out) + ((static_cast<long long>(b) * p.T_ + tok) * p.Hq + hq) * D + at;
 #pragma unroll
-  for (int v = 0; v < V; v += 2) store2(dst + v, num[v] * inv, num[v + 1] * inv);
+  for (int v = 0; v < V; v += 2) store2(dst + v, sum.num[v] * inv, sum.num[v + 1] * inv);
 }
 
 }  // namespace kv4

@@ -1655,7 +1655,7 @@ sambay_status kv4_rows_launch(bool write, sambay::kv4::RowParams<T>& p, cudaStre
   auto kern = write ? kv4_write_kernel<T, D> : kv4_read_kernel<T, D>;
   ProfScope ps(write ? "kv4_write" : "kv4_read", st);
   return launch_k(kern, dim3(p.head_ctas * static_cast<unsigned>((p.groups + deep - 1) / deep), p.pg.B), dim3(32 * kRowWarps), 0, st,
-                  false, 1, p) == cudaSuccess
+                  true, 1, p) == cudaSuccess
              ? SAMBAY_OK
              : SAMBAY_ERR_CUDA;
 }
@@ -1688,7 +1688,7 @@ constexpr int kKv4MaxTokens = 16;
 struct Kv4Plan {
   int nt = 1, row_tiles = 1, cols = 8, grid = 0;
   bool one_tile = false;       // no pair has more than one tile: nothing is shared
-  bool many = false;           // about how many parts a pair has
+  bool many = false;           // several CTAs combine a row
   size_t ml_part = 0, total = 0;
 };
 
@@ -1705,7 +1705,10 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   if (pairs > 0x7FFFFFFFLL / tiles) return pl;          // grid 0: the line of tiles is too long
   pl.grid = static_cast<int>(std::min(static_cast<long long>(kSplitTarget) * ctas, pairs * tiles));
   pl.one_tile = tiles == 1;
-  pl.many = pl.grid * static_cast<long long>(sambay::kv4::kWarps) > 8 * pairs;
+  // a row of many parts is combined by several CTAs, where they all run at once
+  // (8 x 4097 tokens, 4 queries: 30.4 us that way in 2560 CTAs, 26.5 us by warps)
+  pl.many = pl.grid * static_cast<long long>(sambay::kv4::kWarps) > 8 * pairs &&
+            static_cast<long long>(d->batch) * q_heads * tokens * (d->head_dim / 32) <= 4 * kSplitTarget;
   if (!pl.one_tile) {
     const size_t parts = static_cast<size_t>(pl.grid) * sambay::kv4::kWarps * 2 * pl.cols;
     pl.ml_part = round256(parts * d->head_dim * 4);
@@ -1728,13 +1731,13 @@ sambay_status kv4_attn_launch(int dev, const sambay::kv4::AttnParams& p, const K
   }
   {
     ProfScope ps("kv4_attn", st);
-    if (launch_k(kern, dim3(pl.grid), dim3(kThreads), kAttnSmem, st, false, 1, p) != cudaSuccess) return SAMBAY_ERR_CUDA;
+    if (launch_k(kern, dim3(pl.grid), dim3(kThreads), kAttnSmem, st, true, 1, p) != cudaSuccess) return SAMBAY_ERR_CUDA;
   }
   if (!pl.one_tile) {
-    const long long rows = static_cast<long long>(p.pg.B) * p.T_ * p.Hq;
+    const int rows = p.T_ * p.Hq;
     ProfScope ps("kv4_combine", st);
-    if (launch_k(pl.many ? kv4_combine_kernel<T, D, NT, 8> : kv4_combine_kernel<T, D, NT, 1>,
-                 dim3(static_cast<unsigned>(pl.many ? rows : (rows + 7) / 8)), dim3(256), 0, st, true, 1,
+    if (launch_k(pl.many ? kv4_combine_kernel<T, D, NT, true> : kv4_combine_kernel<T, D, NT, false>,
+                 dim3(pl.many ? rows * (D / 32) : (rows + 7) / 8, p.pg.B), dim3(256), 0, st, true, 1,
                  p) != cudaSuccess)
       return SAMBAY_ERR_CUDA;
   }
@@ -1835,6 +1838,7 @@ sambay_status sambay_cross_attn_decode_kv4(const sambay_kv4_cache* c, const samb
   p.T_ = tokens;
   p.Hq = q_heads;
   p.G = q_heads / d->kv_heads;
+  p.group_inv = (65536 + p.G - 1) / p.G;
   p.row_tiles = pl.row_tiles;
   p.cols = pl.cols;
   p.warps = pl.grid * sambay::kv4::kWarps;
