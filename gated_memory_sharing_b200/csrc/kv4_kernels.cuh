@@ -552,7 +552,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 2;                       // of a warp's ring,
 constexpr int kStageTiles = 2;                   // two tiles each
 constexpr int kTileBytes = 4608;
-constexpr int kAttnSmem = kWarps * kStages * (kStageTiles * kTileBytes + 8);      // three times this fit an SM
+constexpr int kScaleBytes = 512;                 // a tile's scales of K, then of V, as f16
+constexpr int kWarpSmem = kStages * kStageTiles * kTileBytes + kScaleBytes;
+constexpr int kAttnSmem = kWarps * (kWarpSmem + kStages * 8);      // three times this fit an SM
 constexpr long long kWaitCycles = 1LL << 31;     // a copy that has not come after about a second
 // Probabilities are kept times 2^15 (the largest of a row is 2^15): as f16 they
 // then have 11 bits down to 2^-29 of the largest instead of 2^-14, which shows
@@ -775,6 +777,12 @@ __device__ __forceinline__ Line begin_of(const AttnParams& p, int gw, Cursor& c,
   return line;
 }
 
+// This thread's 128 bytes of an array, to L2.
+__device__ __forceinline__ void prefetch_part(const void* p, long long bytes) {
+  const long long at = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) * 128;
+  if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p) + at));
+}
+
 // Query row r of a (sequence, KV head): token r / G, head r % G of the group.
 // The MMAs compute S^T = K Q^T and O^T = V^T P^T: tokens (values) are the 16
 // rows of A, straight from the cache's layout, and 8 query rows the columns.
@@ -793,12 +801,17 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   const int g = lane >> 2, t = lane & 3;
   // the first warps of all CTAs, then their second ones: few shares spread over the GPU
   const int gw = warp * gridDim.x + blockIdx.x;
-  uint8_t* ring = smem + warp * (S * kStageBytes);
+  uint8_t* ring = smem + warp * kWarpSmem;
+  uint8_t* scales = ring + S * kStageBytes;
   const uint32_t ring_addr = shared_addr(ring);
-  const uint32_t bars = shared_addr(smem + kWarps * S * kStageBytes) + warp * (S * 8);
+  const uint32_t bars = shared_addr(smem + kWarps * kWarpSmem) + warp * (S * 8);
 
   pdl_wait();
   pdl_launch_dependents();             // the combine kernel's CTAs come as this one's leave
+  // The lengths say which pages and queries a warp needs; meanwhile all of the
+  // table and the queries come to L2 (as far as the grid's threads reach).
+  prefetch_part(pg.table, static_cast<long long>(pg.B) * pg.table_pages * 4);
+  prefetch_part(p.q, static_cast<long long>(pg.B) * p.T_ * p.Hq * D * sizeof(T));
   Cursor c{};                          // the tile being worked on
   int begin = 0;
   const Line line = begin_of<D>(p, gw, c, &begin);
@@ -869,7 +882,9 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
           raw[n][ks].zero();
     }
   };
-  fetch();                             // on their way while the first pages are looked up
+  // where registers allow: on their way while the first pages are looked up
+  constexpr bool kEarly = NT == 1 && !SPLIT;
+  if (kEarly) fetch();
   issue(0);
 
   uint32_t qb[NQ][NT][KS][2];
@@ -885,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
     if (loaded < share) issue(st ^ 1);
     if (fresh) {
       // B fragments of Q (column g of n-tile n), and per accumulator column its factor and its last token
-      if (i > 0) fetch();
+      if (!kEarly || i > 0) fetch();
       fresh = false;
       lim_min = c.len;
 #pragma unroll
@@ -949,30 +964,38 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
     // One tile.  EDGE: not every column sees all of its tokens, or some are missing.
     auto tile = [&](int tok0, const uint8_t* base, uint32_t here, auto edge) {
       constexpr bool EDGE = decltype(edge)::value;
+      // The tile's scales, 8 of K (`first` kKs) or V (kVs) converted a lane: every
+      // lane needs 1/4 (K) or 1/8 (V) of them, which they would convert 8 and 4 times over.
+      auto stage_scales = [&](int first) {
+        const uint2 v = *reinterpret_cast<const uint2*>(base + lane * 8 / D * Block<D>::kBytes + first + lane * 8 % D);
+        uint4 h;
+        e4m3x4_f16x2(v.x, h.x, h.y);
+        e4m3x4_f16x2(v.y, h.z, h.w);
+        __syncwarp();
+        *reinterpret_cast<uint4*>(scales + lane * 16) = h;
+        __syncwarp();
+      };
+      stage_scales(Block<D>::kKs);
       // S^T of group q: entries 0, 1: token g, columns 2t, 2t + 1; entries 2, 3: token g + 8
       float s[NT][GP][4];
 #pragma unroll
       for (int q = 0; q < GP; ++q) {
         const uint8_t* grp = base + q * Block<D>::kBytes;
         if (!EDGE || (here >> q & 1)) {
-          uint32_t kc[KS], sc[2][KS / 4];
+          uint32_t kc[KS], sl[2][KS / 2];              // sl: tokens g and g + 8, two blocks each
 #pragma unroll
           for (int k = 0; k < KS / 4; ++k) {
             const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kK + k * 512 + lane * 16);
             kc[4 * k] = v.x; kc[4 * k + 1] = v.y; kc[4 * k + 2] = v.z; kc[4 * k + 3] = v.w;
-          }
-          if (KS == 4) {
-            const uint2 v = *reinterpret_cast<const uint2*>(grp + Block<D>::kKs + g * 8);
-            sc[0][0] = v.x; sc[1][0] = v.y;
-          } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kKs + g * 16);
-            sc[0][0] = v.x; sc[0][KS / 4 - 1] = v.y; sc[1][0] = v.z; sc[1][KS / 4 - 1] = v.w;
+            const uint4 u = *reinterpret_cast<const uint4*>(scales + (q * D + g * (2 * KS)) * 2 + k * 16);
+            if (KS == 4) {
+              sl[0][0] = u.x; sl[0][1] = u.y; sl[1][0] = u.z; sl[1][1] = u.w;
+            } else {
+              sl[k][0] = u.x; sl[k][1] = u.y; sl[k][KS / 2 - 2] = u.z; sl[k][KS / 2 - 1] = u.w;
+            }
           }
 #pragma unroll
           for (int k = 0; k < KS / 4; ++k) {
-            uint32_t sl[2][2];
-            e4m3x4_f16x2(sc[0][k], sl[0][0], sl[0][1]);
-            e4m3x4_f16x2(sc[1][k], sl[1][0], sl[1][1]);
 #pragma unroll
             for (int bp = 0; bp < 2; ++bp) {           // blocks 4k + 2 bp, + 1
               uint32_t x0[4], x1[4];                   // tokens g and g + 8
@@ -980,8 +1003,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
               e2m1x8_f16x2(kc[4 * k + 2 + bp], x1);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t a0 = mul_f16x2_half(x0[2 * e], sl[0][bp], e), a1 = mul_f16x2_half(x1[2 * e], sl[1][bp], e);
-                const uint32_t a2 = mul_f16x2_half(x0[2 * e + 1], sl[0][bp], e), a3 = mul_f16x2_half(x1[2 * e + 1], sl[1][bp], e);
+                const uint32_t a0 = mul_f16x2_half(x0[2 * e], sl[0][2 * k + bp], e), a1 = mul_f16x2_half(x1[2 * e], sl[1][2 * k + bp], e);
+                const uint32_t a2 = mul_f16x2_half(x0[2 * e + 1], sl[0][2 * k + bp], e), a3 = mul_f16x2_half(x1[2 * e + 1], sl[1][2 * k + bp], e);
                 const int kb = 4 * k + 2 * bp + e;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -1039,6 +1062,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
           }
         }
       }
+      stage_scales(Block<D>::kVs);
 #pragma unroll
       for (int q = 0; q < GP; ++q) {
         if (EDGE && !(here >> q & 1)) continue;
@@ -1069,18 +1093,18 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
         // sequence's are blanked, whose P is 0 (0 x NaN is not), and a block of
         // NaN reaches only the columns that see its token: its scale is blanked
         // too, and these columns are set to NaN.
-        uint32_t keep = 0xFFFFFFFFu;
+        uint32_t keep_lo = 0, keep_hi = 0;           // halves of the sequence's own tokens 2t, 2t + 1 and 2t + 8, 2t + 9
         if (EDGE) {
-          keep = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (tok + 2 * t + (e & 1) + 8 * (e >> 1) < c.len) keep |= 0xFFu << (8 * e);
+          const int left = c.len - tok - 2 * t;
+          keep_lo = left > 1 ? 0xFFFFFFFFu : left > 0 ? 0xFFFFu : 0u;
+          keep_hi = left > 9 ? 0xFFFFFFFFu : left > 8 ? 0xFFFFu : 0u;
         }
 #pragma unroll
         for (int k = 0; k < KS / 4; ++k) {
           const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kV + k * 512 + lane * 16);
-          const uint4 sv = *reinterpret_cast<const uint4*>(grp + Block<D>::kVs + t * (D / 4) + k * 16);
-          uint32_t scw[4] = {sv.x & keep, sv.y & keep, sv.z & keep, sv.w & keep};
+          const uint4* sv = reinterpret_cast<const uint4*>(scales + (q * D + t * (4 * KS) + k * 16) * 2);
+          const uint4 s01 = sv[0], s23 = sv[1];
+          uint32_t lo[4] = {s01.x, s01.z, s23.x, s23.z}, hi[4] = {s01.y, s01.w, s23.y, s23.w};
           uint32_t x0[4], x1[4], x2[4], x3[4];
           e2m1x8_f16x2(v.x, x0);       // values 2g, tokens 2t, 2t + 1
           e2m1x8_f16x2(v.y, x1);       // values 2g + 1
@@ -1090,18 +1114,21 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
           for (int e = 0; e < 4; ++e) {
             int bad = 0x7FFFFFFF;                     // first token of the group whose block is NaN
             if (EDGE) {
-              const uint32_t nan = __vcmpeq4(scw[e], 0x7F7F7F7Fu);
-              if (__any_sync(0xFFFFFFFFu, nan != 0)) {
-                scw[e] &= ~nan;
-                if (nan) bad = tok + 2 * t + (nan & 0xFFu ? 0 : nan & 0xFF00u ? 1 : nan & 0xFF0000u ? 8 : 9);
+              lo[e] &= keep_lo;
+              hi[e] &= keep_hi;
+              // a scale's f16 is at most 0x5F00, a NaN's over 0x7C00
+              const uint32_t nan_lo = __vcmpgtu2(lo[e] & 0x7FFF7FFFu, 0x7C007C00u), nan_hi = __vcmpgtu2(hi[e] & 0x7FFF7FFFu, 0x7C007C00u);
+              if (__any_sync(0xFFFFFFFFu, (nan_lo | nan_hi) != 0)) {
+                lo[e] &= ~nan_lo;
+                hi[e] &= ~nan_hi;
+                if (nan_lo | nan_hi)
+                  bad = tok + 2 * t + (nan_lo & 0xFFFFu ? 0 : nan_lo ? 1 : nan_hi & 0xFFFFu ? 8 : 9);
                 bad = min(bad, __shfl_xor_sync(0xFFFFFFFFu, bad, 1));
                 bad = min(bad, __shfl_xor_sync(0xFFFFFFFFu, bad, 2));
               }
             }
-            uint32_t slo, shi;
-            e4m3x4_f16x2(scw[e], slo, shi);
-            const uint32_t a0 = mul_f16x2(x0[e], slo), a1 = mul_f16x2(x1[e], slo);
-            const uint32_t a2 = mul_f16x2(x2[e], shi), a3 = mul_f16x2(x3[e], shi);
+            const uint32_t a0 = mul_f16x2(x0[e], lo[e]), a1 = mul_f16x2(x1[e], lo[e]);
+            const uint32_t a2 = mul_f16x2(x2[e], hi[e]), a3 = mul_f16x2(x3[e], hi[e]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
@@ -1182,76 +1209,104 @@ struct RowSum {
 };
 
 // Rows whose pair was shared by several warps, from their parts in the line's
-// order.  Grid (rows of a sequence or slices of them, sequences).
-//   MANY = false: a warp a row, D / 32 values a lane.
-//   MANY: a CTA for 32 values of a row; 8 lanes take 4 values each, 32 of them
-//   every 32nd part, and then their sums are added in order.
-template <typename T, int D, int NT, bool MANY>
+// order.  Grid y: sequences.
+//   COLS > 0: a warp for COLS columns of a pair, D / 32 values a lane.
+//   COLS = 0: a CTA for 32 values of a row; 8 lanes take 4 values each, 32 of
+//   them every 32nd part, and then their sums are added in order.
+template <typename T, int D, int NT, int COLS>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
-  constexpr int V = MANY ? 4 : D / 32, SLICES = MANY ? D / 32 : 1;
+  constexpr bool MANY = COLS == 0;
+  constexpr int kCols = MANY ? 1 : COLS;
+  constexpr int V = MANY ? 4 : D / 32, SLICES = D / 32;
   const Pages& pg = p.pg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = MANY ? blockIdx.x / SLICES : blockIdx.x * 8 + warp, b = blockIdx.y;
-  const int tok = row / p.Hq, hq = row - tok * p.Hq;
-  const int h = hq / p.G, r = tok * p.G + hq - h * p.G;
-  const int pair = h * p.row_tiles + r / (8 * NT), col = r % (8 * NT);
-  const int at = MANY ? blockIdx.x % SLICES * 32 + (threadIdx.x & 7) * 4 : lane * V;       // first of the lane's values
+  const int b = blockIdx.y;
+  // the pair, its first column here, and the lane's first value
+  const unsigned u = MANY ? blockIdx.x / SLICES : blockIdx.x * 8 + warp;
+  const unsigned per = (p.cols + kCols - 1) / kCols;
+  const int pair = u / per, col0 = (u - pair * per) * kCols;
+  const int at = MANY ? blockIdx.x % SLICES * 32 + (threadIdx.x & 7) * 4 : lane * V;
+  const int h = p.row_tiles == 1 ? pair : pair / p.row_tiles, rt = pair - h * p.row_tiles;
+  const bool in = h < pg.Hkv;
   int before;
   const Line line = line_of<D>(p, b, &before);
   const int tiles = tiles_of<D>(len_of<true>(p, b, false));
-  const int a = before + pair * tiles;
+  const int a = before + (in ? pair : 0) * tiles;
   const int w0 = line.share_of(a), w1 = line.share_of(a + tiles - 1);
   const int first = line.begin(w0) == a ? 0 : 1;
-  const bool live = tok < rows_of<true>(p.count, b, p.T_, false);
-  const float ve = pow2i(head_exp<true>(pg.v_exp, min(h, pg.Hkv - 1)));
+  const int rows = rows_of<true>(p.count, b, p.T_, false) * p.G;       // real ones of a KV head
+  const float ve = pow2i(head_exp<true>(pg.v_exp, in ? h : 0));
   // what was read so far no kernel of this call writes; every thread waits, so
   // that this kernel does not end before the one whose parts it reads
   pdl_wait();
-  pdl_launch_dependents();
-  if (!live || w0 == w1) return;       // the whole CTA's where MANY; w0 == w1: finished by that warp
+  if (!in || w0 == w1) return;         // w0 == w1: finished by that warp
+  // row r of the KV head: where it goes
+  auto store = [&](const RowSum<V>& sum, int r) {
+    const float inv = sum.den == 0.0f ? 0.0f : ve / sum.den;
+    const int tok = r * p.group_inv >> 16;
+    T* dst = static_cast<T*>(p.out) + ((static_cast<long long>(b) * p.T_ + tok) * p.Hq + h * p.G + r - tok * p.G) * D + at;
+#pragma unroll
+    for (int v = 0; v < V; v += 2) store2(dst + v, sum.num[v] * inv, sum.num[v + 1] * inv);
+  };
+  const int r0 = rt * (8 * NT) + col0;
+  if (!MANY) {
+    RowSum<V> sum[kCols];
+#pragma unroll kCols == 1 ? 4 : 2
+    for (int w = w0; w <= w1; ++w) {
+      const long long k = (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col0;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        if (r0 + c < rows && col0 + c < p.cols) {
+          const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + (k + c) * 2);
+          float x[V];
+#pragma unroll
+          for (int v = 0; v < V; v += 2) load2(p.o_part + (k + c) * D + at + v, x + v);
+          sum[c].add(ml.x, ml.y, x);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+      if (r0 + c < rows && col0 + c < p.cols) store(sum[c], r0 + c);
+    return;
+  }
+  if (r0 >= rows) return;              // the whole CTA's
   RowSum<V> sum;
-  const int step = MANY ? 32 : 1;
 #pragma unroll 4
-  for (int w = w0 + (MANY ? threadIdx.x >> 3 : 0); w <= w1; w += step) {
-    const long long k = (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col;
+  for (int w = w0 + (threadIdx.x >> 3); w <= w1; w += 32) {
+    const long long k = (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col0;
     const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + k * 2);
     float x[V];
 #pragma unroll
     for (int v = 0; v < V; v += 2) load2(p.o_part + k * D + at + v, x + v);
     sum.add(ml.x, ml.y, x);
   }
-  if (MANY) {
-    // the four of a warp, then the warps
+  // the four of a warp, then the warps
 #pragma unroll
-    for (int o = 8; o < 32; o <<= 1) {
-      float x[V];
+  for (int o = 8; o < 32; o <<= 1) {
+    float x[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = __shfl_xor_sync(0xFFFFFFFFu, sum.num[v], o);
-      sum.add(__shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.den, o), x);
-    }
-    __shared__ float sh[8][8][V + 2];
-    if (lane < 8) {
-      float* mine = sh[warp][lane];
-      mine[V] = sum.m;
-      mine[V + 1] = sum.den;
-#pragma unroll
-      for (int v = 0; v < V; ++v) mine[v] = sum.num[v];
-    }
-    __syncthreads();
-    if (threadIdx.x >= 8) return;
-#pragma unroll
-    for (int k = 1; k < 8; ++k) {
-      const float* other = sh[k][lane];
-      float x[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = other[v];
-      sum.add(other[V], other[V + 1], x);
-    }
+    for (int v = 0; v < V; ++v) x[v] = __shfl_xor_sync(0xFFFFFFFFu, sum.num[v], o);
+    sum.add(__shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.den, o), x);
   }
-  const float inv = sum.den == 0.0f ? 0.0f : ve / sum.den;
-  T* dst = static_cast<T*>(p.out) + ((static_cast<long long>(b) * p.T_ + tok) * p.Hq + hq) * D + at;
+  __shared__ float sh[8][8][V + 2];
+  if (lane < 8) {
+    float* mine = sh[warp][lane];
+    mine[V] = sum.m;
+    mine[V + 1] = sum.den;
 #pragma unroll
-  for (int v = 0; v < V; v += 2) store2(dst + v, sum.num[v] * inv, sum.num[v + 1] * inv);
+    for (int v = 0; v < V; ++v) mine[v] = sum.num[v];
+  }
+  __syncthreads();
+  if (threadIdx.x >= 8) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    const float* other = sh[k][lane];
+    float x[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = other[v];
+    sum.add(other[V], other[V + 1], x);
+  }
+  store(sum, r0);
 }
 
 }  // namespace kv4

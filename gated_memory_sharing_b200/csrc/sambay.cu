@@ -1688,7 +1688,7 @@ constexpr int kKv4MaxTokens = 16;
 struct Kv4Plan {
   int nt = 1, row_tiles = 1, cols = 8, grid = 0;
   bool one_tile = false;       // no pair has more than one tile: nothing is shared
-  bool many = false;           // several CTAs combine a row
+  int combine_cols = 1;        // rows that a warp of the combine kernel takes; 0: several CTAs a row
   size_t ml_part = 0, total = 0;
 };
 
@@ -1705,10 +1705,13 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   if (pairs > 0x7FFFFFFFLL / tiles) return pl;          // grid 0: the line of tiles is too long
   pl.grid = static_cast<int>(std::min(static_cast<long long>(kSplitTarget) * ctas, pairs * tiles));
   pl.one_tile = tiles == 1;
-  // a row of many parts is combined by several CTAs, where they all run at once
-  // (8 x 4097 tokens, 4 queries: 30.4 us that way in 2560 CTAs, 26.5 us by warps)
-  pl.many = pl.grid * static_cast<long long>(sambay::kv4::kWarps) > 8 * pairs &&
-            static_cast<long long>(d->batch) * q_heads * tokens * (d->head_dim / 32) <= 4 * kSplitTarget;
+  // Parts of a pair (about): few, and many rows: a warp joins 4 rows (64 x 2048
+  // tokens at 320 heads: 15 us, by single rows 22 us); more: a row (8 x 4097
+  // tokens, 4 queries: 11 us, by 4 rows 26 us); many, of rows few enough for all
+  // CTAs to run at once: several CTAs a row (3 x 8191 f32: 9 us, by warps 14 us).
+  const long long warps = pl.grid * static_cast<long long>(sambay::kv4::kWarps);
+  const bool at_once = static_cast<long long>(d->batch) * q_heads * tokens * (d->head_dim / 32) <= 4 * kSplitTarget;
+  pl.combine_cols = warps <= 2 * pairs && pl.cols >= 4 ? 4 : warps > 8 * pairs && at_once ? 0 : 1;
   if (!pl.one_tile) {
     const size_t parts = static_cast<size_t>(pl.grid) * sambay::kv4::kWarps * 2 * pl.cols;
     pl.ml_part = round256(parts * d->head_dim * 4);
@@ -1734,11 +1737,14 @@ sambay_status kv4_attn_launch(int dev, const sambay::kv4::AttnParams& p, const K
     if (launch_k(kern, dim3(pl.grid), dim3(kThreads), kAttnSmem, st, true, 1, p) != cudaSuccess) return SAMBAY_ERR_CUDA;
   }
   if (!pl.one_tile) {
-    const int rows = p.T_ * p.Hq;
+    auto k0 = kv4_combine_kernel<T, D, NT, 0>, k1 = kv4_combine_kernel<T, D, NT, 1>, k4 = kv4_combine_kernel<T, D, NT, 4>;
+    SAMBAY_MAX_CARVEOUT(k0, dev);
+    SAMBAY_MAX_CARVEOUT(k1, dev);
+    SAMBAY_MAX_CARVEOUT(k4, dev);
+    const int cols = pl.combine_cols, pairs = p.pg.Hkv * p.row_tiles;
+    const int grid = cols == 0 ? pairs * p.cols * (D / 32) : (pairs * ((p.cols + cols - 1) / cols) + 7) / 8;
     ProfScope ps("kv4_combine", st);
-    if (launch_k(pl.many ? kv4_combine_kernel<T, D, NT, true> : kv4_combine_kernel<T, D, NT, false>,
-                 dim3(pl.many ? rows * (D / 32) : (rows + 7) / 8, p.pg.B), dim3(256), 0, st, true, 1,
-                 p) != cudaSuccess)
+    if (launch_k(cols == 0 ? k0 : cols == 1 ? k1 : k4, dim3(grid, p.pg.B), dim3(256), 0, st, true, 1, p) != cudaSuccess)
       return SAMBAY_ERR_CUDA;
   }
   return SAMBAY_OK;
