@@ -661,28 +661,37 @@ __device__ __forceinline__ int len_of(const AttnParams& p, int b, bool tell) {
 template <int D>
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + 4096 / D - 1) / (4096 / D)); }
 
-// The line: its length in tiles (below 2^31, the host sees to it) and the warps
-// that share it, none of them without a tile: share w has `base` tiles, or one
-// more (the first `rem` of them).
+// The line is measured in units, one a tile and, where shares are long, kSwitch
+// more in front of each pair's first: what changing to a pair costs a warp (a
+// batch with empty and short sequences would else leave some warps with many
+// of them: 37 sequences of 0 .. 5000 tokens took 37 us).  Its length (below
+// 2^31, the host sees to it) is cut into shares, none without a tile: share w
+// has `base` units, or one more (the first `rem` of them).
+constexpr int kSwitch = 2;
 struct Line {
   int shares, base, rem;
+  int gap;                 // units in front of a pair
   __device__ __forceinline__ int begin(int w) const { return w * base + min(w, rem); }
-  // the share that holds tile x
+  // the share that holds unit x
   __device__ __forceinline__ int share_of(int x) const {
     const int cut = rem * (base + 1);
     return x < cut ? x / (base + 1) : rem + (x - cut) / base;
   }
 };
 
+// tiles: of one pair of every sequence
 __device__ __forceinline__ Line make_line(const AttnParams& p, int tiles) {
+  const int pairs = p.pg.Hkv * p.row_tiles;
   Line line;
-  line.shares = min(tiles, p.warps);
-  line.base = static_cast<unsigned>(tiles) / static_cast<unsigned>(line.shares);
-  line.rem = tiles - line.base * line.shares;
+  line.gap = tiles * pairs >= 4 * p.warps ? kSwitch : 0;
+  const int units = (tiles + line.gap * p.pg.B) * pairs;
+  line.shares = min(units, p.warps);
+  line.base = static_cast<unsigned>(units) / static_cast<unsigned>(line.shares);
+  line.rem = units - line.base * line.shares;
   return line;
 }
 
-// The line of a call, and the tile in it at which sequence b begins (one warp of
+// The line of a call, and the unit in it at which sequence b begins (one warp of
 // the combine kernel).
 template <int D>
 __device__ __forceinline__ Line line_of(const AttnParams& p, int b, int* before) {
@@ -692,9 +701,9 @@ __device__ __forceinline__ Line line_of(const AttnParams& p, int b, int* before)
     s += n;
     if (i < b) sb += n;
   }
-  const int pairs = p.pg.Hkv * p.row_tiles;
-  *before = __reduce_add_sync(0xFFFFFFFFu, sb) * pairs;
-  return make_line(p, __reduce_add_sync(0xFFFFFFFFu, s) * pairs);
+  const Line line = make_line(p, __reduce_add_sync(0xFFFFFFFFu, s));
+  *before = (static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, sb)) + line.gap * b) * p.pg.Hkv * p.row_tiles;
+  return line;
 }
 
 // A place in the line.
@@ -732,11 +741,12 @@ __device__ __forceinline__ int scan(int v) {
   return v;
 }
 
-// The line, and the place in it where share gw begins (one warp; the place of
-// a share that is none is not set).  A lane sums the tiles of B / 32 sequences;
-// then the sequences of the lane that holds the place are looked through.
+// The place in the line where share gw begins, and the units from there to its
+// end: 0 where the share is none (one warp).  A lane sums the tiles of B / 32
+// sequences; then the sequences of the lane that holds the place are looked
+// through.  *gap: the line's.
 template <int D>
-__device__ __forceinline__ Line begin_of(const AttnParams& p, int gw, Cursor& c, int* begin) {
+__device__ __forceinline__ int begin_of(const AttnParams& p, int gw, Cursor& c, int* gap) {
   const int lane = threadIdx.x & 31;
   const int pairs = p.pg.Hkv * p.row_tiles, per = (p.pg.B + 31) >> 5;
   int mine = 0, len = 0;
@@ -744,19 +754,22 @@ __device__ __forceinline__ Line begin_of(const AttnParams& p, int gw, Cursor& c,
     len = len_of(p, i, gw == 0);
     mine += tiles_of<D>(len);
   }
-  const int upto = scan(mine);                       // tiles of one pair of these sequences and those before
-  const Line line = make_line(p, __shfl_sync(0xFFFFFFFFu, upto, 31) * pairs);
-  if (gw >= line.shares) return line;
-  *begin = line.begin(gw);
-  int x = *begin;
+  int upto = scan(mine);                             // tiles of one pair of these sequences and those before
+  const Line line = make_line(p, __shfl_sync(0xFFFFFFFFu, upto, 31));
+  *gap = line.gap;
+  if (gw >= line.shares) return 0;
+  int x = line.begin(gw);
+  int left = line.begin(gw + 1) - x;
+  int before = upto - mine + line.gap * min(p.pg.B, lane * per);
+  upto += line.gap * min(p.pg.B, lane * per + per);
   int k = __ffs(__ballot_sync(0xFFFFFFFFu, upto * pairs > x)) - 1;
-  x -= __shfl_sync(0xFFFFFFFFu, upto - mine, k) * pairs;
+  x -= __shfl_sync(0xFFFFFFFFu, before, k) * pairs;
   c.b = k;
   if (per > 1) {
     for (int b0 = k * per;; b0 += 32) {              // ends: x is in the line
       const int i = b0 + lane;
       len = i < p.pg.B ? len_of(p, i, false) : 0;
-      mine = i < p.pg.B ? tiles_of<D>(len) : 0;
+      mine = i < p.pg.B ? tiles_of<D>(len) + line.gap : 0;
       const int sum = scan(mine);
       const unsigned past = __ballot_sync(0xFFFFFFFFu, sum * pairs > x);
       if (past) {
@@ -770,11 +783,14 @@ __device__ __forceinline__ Line begin_of(const AttnParams& p, int gw, Cursor& c,
   }
   c.len = __shfl_sync(0xFFFFFFFFu, len, k);
   c.tiles = tiles_of<D>(c.len);
-  const int pair = static_cast<unsigned>(x) / static_cast<unsigned>(c.tiles);
-  c.tile = x - pair * c.tiles;
+  const int units = c.tiles + line.gap;
+  const int pair = static_cast<unsigned>(x) / static_cast<unsigned>(units);
+  x -= pair * units + line.gap;
+  c.tile = max(0, x);
+  left += min(0, x);                                 // a share that begins in a pair's gap
   c.h = p.row_tiles == 1 ? pair : pair / p.row_tiles;
   c.rt = pair - c.h * p.row_tiles;
-  return line;
+  return left;
 }
 
 // This thread's 128 bytes of an array, to L2.
@@ -806,17 +822,18 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   const uint32_t ring_addr = shared_addr(ring);
   const uint32_t bars = shared_addr(smem + kWarps * kWarpSmem) + warp * (S * 8);
 
+  // The lengths say which pages and queries a warp needs; meanwhile (and while
+  // the kernel in front finishes) they, the table and the queries come to L2, as
+  // far as the grid's threads reach.
+  prefetch_part(p.lens, 4LL * pg.B);
+  prefetch_part(pg.table, 4LL * pg.B * pg.table_pages);
+  prefetch_part(p.q, static_cast<long long>(pg.B) * p.T_ * p.Hq * D * sizeof(T));
   pdl_wait();
   pdl_launch_dependents();             // the combine kernel's CTAs come as this one's leave
-  // The lengths say which pages and queries a warp needs; meanwhile all of the
-  // table and the queries come to L2 (as far as the grid's threads reach).
-  prefetch_part(pg.table, static_cast<long long>(pg.B) * pg.table_pages * 4);
-  prefetch_part(p.q, static_cast<long long>(pg.B) * p.T_ * p.Hq * D * sizeof(T));
   Cursor c{};                          // the tile being worked on
-  int begin = 0;
-  const Line line = begin_of<D>(p, gw, c, &begin);
-  if (gw >= line.shares) return;
-  const int share = line.begin(gw + 1) - begin;
+  int gap;
+  int left = begin_of<D>(p, gw, c, &gap);      // units of the share that are still to be worked on
+  if (left <= 0) return;
   if (lane < S) bar_init(bars + 8 * lane);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
@@ -827,13 +844,13 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   int page = -1;
   bool window = true;                  // to be loaded
   uint32_t have = 0;                   // SG bits a stage: which groups were loaded
-  int loaded = 0;                      // tiles of the share that are on their way or here
+  int to_load = left;                  // ... to be asked for
   // The tiles that a stage takes at a place: two of one pair, from an even one on.
-  auto step_of = [&](const Cursor& x, int left) {
-    return (x.tile & 1) ? 1 : min(min(kStageTiles, left), x.tiles - x.tile);
+  auto step_of = [&](const Cursor& x, int units) {
+    return (x.tile & 1) ? 1 : min(min(kStageTiles, units), x.tiles - x.tile);
   };
   auto issue = [&](int st) {
-    const int n = step_of(in, share - loaded);
+    const int n = step_of(in, to_load);
     const int tok = in.tile * TILE + lane * kGroup;
     if (window || in.tile % WIN == 0) {
       window = false;
@@ -859,16 +876,17 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
     if (piece && (lane & p.piece_low) == 0)
       bulk_load(ring_addr + st * kStageBytes + lane * Block<D>::kBytes, src, __popc(piece) * Block<D>::kBytes, bar);
     have = (have & ~(((1u << SG) - 1) << (SG * st))) | mask << (SG * st);
-    loaded += n;
     window = advance<D>(p, in, n);
+    to_load -= window ? n + gap : n;
   };
   // The queries of a pair, as they lie there: column g's values 16 b + 4 t .. + 3.
   Four<T> raw[NT][KS];
-  int nq = 0, kexp = 0;                // query tokens of the sequence; the head's exponent
+  int nq = 0, kexp = 0, vexp = 0;      // query tokens of the sequence; the head's exponents
   auto fetch = [&]() {
     const int row0 = c.rt * (8 * NT);
     nq = rows_of(p.count, c.b, p.T_, c.h == 0 && row0 == 0);
     kexp = head_exp(pg.k_exp, c.h);
+    vexp = head_exp(pg.v_exp, c.h);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = row0 + 8 * n + g, tok = r * p.group_inv >> 16;
@@ -876,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
                     ((static_cast<long long>(c.b) * p.T_ + tok) * p.Hq + c.h * p.G + r - tok * p.G) * D + 4 * t;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        if (r < nq * p.G)
+        if (tok < p.T_)                // rows from nq G on are not written, whatever they are
           raw[n][ks].load(qr + 16 * ks);
         else
           raw[n][ks].zero();
@@ -895,9 +913,9 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
   int st = 0, lim_min = 0;
   uint32_t parity = 0;
 
-  for (int i = 0; i < share;) {        // i: tiles done
-    const int n = step_of(c, share - i);
-    if (loaded < share) issue(st ^ 1);
+  for (int i = 0; left > 0;) {         // i: tiles done
+    const int n = step_of(c, left);
+    if (to_load > 0) issue(st ^ 1);
     if (fresh) {
       // B fragments of Q (column g of n-tile n), and per accumulator column its factor and its last token
       if (!kEarly || i > 0) fetch();
@@ -954,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
       // lost: tell, and leave when the copies in flight have come (or again do not)
       record_status(kStatusTimeout);
       bar_wait(bars + 8 * st, parity >> st & 1);
-      if (i + n < loaded) bar_wait(bars + 8 * (st ^ 1), parity >> (st ^ 1) & 1);
+      if (to_load < left - n - (c.tile + n == c.tiles ? gap : 0)) bar_wait(bars + 8 * (st ^ 1), parity >> (st ^ 1) & 1);
       return;
     }
     parity ^= 1u << st;
@@ -966,8 +984,10 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
       constexpr bool EDGE = decltype(edge)::value;
       // The tile's scales, 8 of K (`first` kKs) or V (kVs) converted a lane: every
       // lane needs 1/4 (K) or 1/8 (V) of them, which they would convert 8 and 4 times over.
+      bool nan = false;                // at an edge: one of those staged last (of any token) is NaN
       auto stage_scales = [&](int first) {
         const uint2 v = *reinterpret_cast<const uint2*>(base + lane * 8 / D * Block<D>::kBytes + first + lane * 8 % D);
+        if (EDGE) nan = __any_sync(0xFFFFFFFFu, (__vcmpeq4(v.x, 0x7F7F7F7Fu) | __vcmpeq4(v.y, 0x7F7F7F7Fu)) != 0);
         uint4 h;
         e4m3x4_f16x2(v.x, h.x, h.y);
         e4m3x4_f16x2(v.y, h.z, h.w);
@@ -1116,6 +1136,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
             if (EDGE) {
               lo[e] &= keep_lo;
               hi[e] &= keep_hi;
+            }
+            if (EDGE && nan) {
               // a scale's f16 is at most 0x5F00, a NaN's over 0x7C00
               const uint32_t nan_lo = __vcmpgtu2(lo[e] & 0x7FFF7FFFu, 0x7C007C00u), nan_hi = __vcmpgtu2(hi[e] & 0x7FFF7FFFu, 0x7C007C00u);
               if (__any_sync(0xFFFFFFFFu, (nan_lo | nan_hi) != 0)) {
@@ -1133,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
             for (int n = 0; n < NT; ++n) {
               mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
               if (SPLIT) mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[NQ - 1][n][0], pb[NQ - 1][n][1]);
-              if (EDGE) {
+              if (EDGE && nan) {
 #pragma unroll
                 for (int i2 = 0; i2 < 4; ++i2)
                   if (bad < lim[n][i2 & 1]) o[n][4 * k + e][i2] = __int_as_float(0x7FC00000);
@@ -1155,10 +1177,10 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
     __syncwarp();                      // the stage is read; the next iteration's copies may refill it
     st ^= 1;
 
-    if (c.tile + n == c.tiles || i + n == share) {
+    if (c.tile + n == c.tiles || left == n) {
       // the pair, or this warp's share of it, is done
       const int h = c.h, row0 = c.rt * (8 * NT);
-      const float ve = pow2i(head_exp(pg.v_exp, h));
+      const float ve = pow2i(vexp);
       const bool from_start = i >= c.tile;                     // the pair's first tile is in this share
       const bool done = from_start && c.tile + n == c.tiles;
       // the share's first pair leaves its part in slot 0, its last one in slot 1
@@ -1190,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_ke
         }
       fresh = true;
     }
-    advance<D>(p, c, n);
+    left -= advance<D>(p, c, n) ? n + gap : n;
     i += n;
   }
 }
@@ -1231,9 +1253,9 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
   int before;
   const Line line = line_of<D>(p, b, &before);
   const int tiles = tiles_of<D>(len_of<true>(p, b, false));
-  const int a = before + (in ? pair : 0) * tiles;
-  const int w0 = line.share_of(a), w1 = line.share_of(a + tiles - 1);
-  const int first = line.begin(w0) == a ? 0 : 1;
+  const int a = before + (in ? pair : 0) * (tiles + line.gap);
+  const int w0 = line.share_of(a + line.gap), w1 = line.share_of(a + line.gap + tiles - 1);
+  const int first = line.begin(w0) >= a ? 0 : 1;       // whether the share begins with this pair
   const int rows = rows_of<true>(p.count, b, p.T_, false) * p.G;       // real ones of a KV head
   const float ve = pow2i(head_exp<true>(pg.v_exp, in ? h : 0));
   // what was read so far no kernel of this call writes; every thread waits, so

@@ -1702,7 +1702,7 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   const long long tile = 4096 / d->head_dim;
   const long long tiles = (static_cast<long long>(d->table_pages) * d->page_tokens + tile - 1) / tile;
   const int ctas = sambay::kv4::attn_ctas(d->head_dim, pl.nt, d->io == SAMBAY_F32);
-  if (pairs > 0x7FFFFFFFLL / tiles) return pl;          // grid 0: the line of tiles is too long
+  if (pairs > 0x7FFFFFFFLL / (tiles + sambay::kv4::kSwitch)) return pl;      // grid 0: the line of tiles is too long
   pl.grid = static_cast<int>(std::min(static_cast<long long>(kSplitTarget) * ctas, pairs * tiles));
   pl.one_tile = tiles == 1;
   // Parts of a pair (about): few, and many rows: a warp joins 4 rows (64 x 2048
