@@ -336,7 +336,7 @@ def sambay_cross_attn_decode(dims: AttnDims, q, K, V, out, scale: float, ws, str
 
 
 # The 4-bit cache's calls run once per layer and decoded token, where the
-# host's microseconds show: they pass plain addresses and take the stream as a
+# host's microseconds show: they pass plain addresses, and take the stream as a
 # handle too.
 
 def _a(t):
@@ -344,43 +344,45 @@ def _a(t):
     return None if t is None else t.data_ptr()
 
 
-def _handle(stream):
-    return stream if type(stream) is int else _stream(stream)
-
-
 def make_kv4_cache(pages, table, k_exp=None, v_exp=None) -> Kv4Cache:
     return Kv4Cache(_a(pages), _a(table), _a(k_exp), _a(v_exp))
 
 
 def sambay_kv4_cache_bytes(dims: Kv4Dims) -> int:
-    return load().sambay_kv4_cache_bytes(ctypes.byref(dims))
+    return load().sambay_kv4_cache_bytes(dims)
 
 
 def sambay_kv4_write(cache: Kv4Cache, dims: Kv4Dims, tokens: int, K, V, pos, count=None, k_stride: int = 0,
                      v_stride: int = 0, stream=None):
-    code = load().sambay_kv4_write(ctypes.byref(cache), ctypes.byref(dims), tokens, _a(K), _a(V), k_stride, v_stride,
-                                   _a(pos), _a(count), _handle(stream))
+    code = (_lib or load()).sambay_kv4_write(
+        cache, dims, tokens, None if K is None else K.data_ptr(), None if V is None else V.data_ptr(), k_stride,
+        v_stride, None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(),
+        stream if type(stream) is int else _stream(stream))
     if code:
         raise SambayError("sambay_kv4_write", code)
 
 
 def sambay_kv4_read(cache: Kv4Cache, dims: Kv4Dims, tokens: int, K, V, pos, count=None, stream=None):
-    code = load().sambay_kv4_read(ctypes.byref(cache), ctypes.byref(dims), tokens, _a(K), _a(V), _a(pos), _a(count),
-                                  _handle(stream))
+    code = (_lib or load()).sambay_kv4_read(
+        cache, dims, tokens, None if K is None else K.data_ptr(), None if V is None else V.data_ptr(),
+        None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(),
+        stream if type(stream) is int else _stream(stream))
     if code:
         raise SambayError("sambay_kv4_read", code)
 
 
 def sambay_cross_attn_decode_kv4_workspace(dims: Kv4Dims, q_heads: int, tokens: int) -> int:
-    return load().sambay_cross_attn_decode_kv4_workspace(ctypes.byref(dims), q_heads, tokens)
+    return load().sambay_cross_attn_decode_kv4_workspace(dims, q_heads, tokens)
 
 
 def sambay_cross_attn_decode_kv4(cache: Kv4Cache, dims: Kv4Dims, q_heads: int, tokens: int, q, out, lens, count,
                                  scale: float, ws, ws_bytes=None, stream=None):
     if ws_bytes is None:
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    code = load().sambay_cross_attn_decode_kv4(ctypes.byref(cache), ctypes.byref(dims), q_heads, tokens, _a(q), _a(out),
-                                               _a(lens), _a(count), scale, _a(ws), ws_bytes, _handle(stream))
+    code = (_lib or load()).sambay_cross_attn_decode_kv4(
+        cache, dims, q_heads, tokens, None if q is None else q.data_ptr(), None if out is None else out.data_ptr(),
+        None if lens is None else lens.data_ptr(), None if count is None else count.data_ptr(), scale,
+        None if ws is None else ws.data_ptr(), ws_bytes, stream if type(stream) is int else _stream(stream))
     if code:
         raise SambayError("sambay_cross_attn_decode_kv4", code)
 

@@ -563,10 +563,11 @@ constexpr long long kWaitCycles = 1LL << 31;     // a copy that has not come aft
 constexpr float kPShift = 15.0f;
 constexpr float kNoRef = 3e38f;                  // the exponent offset of a row that has seen nothing
 
-// Resident CTAs an SM: 168 registers a thread suffice for all but the widest
-// variant.  The kernel is bound by what the warp schedulers can dispatch, not
-// by latency: 12, 16 and 20 warps an SM measured the same.
-__host__ __device__ constexpr int attn_ctas(int d, int nt, bool split) { return d * nt * (split ? 2 : 1) <= 256 ? 3 : 2; }
+// Resident CTAs an SM.  The kernel is bound by what the warp schedulers can
+// dispatch, not by latency (12, 16 and 20 warps an SM measured the same), so a
+// variant gets the registers that it needs: 168 a thread for 8 columns, 255 for
+// 16 (168 spill: 64 x 2048 tokens at 16 query heads a KV head 82 us, 255 64 us).
+__host__ __device__ constexpr int attn_ctas(int nt) { return nt == 1 ? 3 : 2; }
 
 struct AttnParams {
   Pages pg;
@@ -805,7 +806,7 @@ __device__ __forceinline__ void prefetch_part(const void* p, long long bytes) {
 // q is scaled per row by a power of two into f16's range (bf16 fits f16's 11
 // bits; with SPLIT (f32 io) it is a pair of f16, 22 bits, and so is P).
 template <typename T, int D, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, attn_ctas(D, NT, SPLIT)) kv4_attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const AttnParams p) {
   constexpr int KS = D / 16;
   constexpr int NQ = SPLIT ? 2 : 1;
   constexpr int TILE = 4096 / D, GP = TILE / kGroup, WIN = 32 / GP;     // WIN: tiles of 32 groups

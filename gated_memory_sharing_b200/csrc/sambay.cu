@@ -1701,7 +1701,7 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   const long long pairs = static_cast<long long>(d->batch) * d->kv_heads * pl.row_tiles;
   const long long tile = 4096 / d->head_dim;
   const long long tiles = (static_cast<long long>(d->table_pages) * d->page_tokens + tile - 1) / tile;
-  const int ctas = sambay::kv4::attn_ctas(d->head_dim, pl.nt, d->io == SAMBAY_F32);
+  const int ctas = sambay::kv4::attn_ctas(pl.nt);
   if (pairs > 0x7FFFFFFFLL / (tiles + sambay::kv4::kSwitch)) return pl;      // grid 0: the line of tiles is too long
   pl.grid = static_cast<int>(std::min(static_cast<long long>(kSplitTarget) * ctas, pairs * tiles));
   pl.one_tile = tiles == 1;

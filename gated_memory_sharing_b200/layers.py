@@ -291,6 +291,12 @@ class Mamba2Scan:
         return m_t
 
 
+# What a call of the 4-bit cache asks for every time, without torch's wrappers.
+_I32 = torch.int32
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 class KV4Cache:
     """The one KV cache of the cross-decoder in 4 bits: rows are quantised as
     they are written (4.5 bits an element), read back, and attended over.
@@ -343,7 +349,7 @@ class KV4Cache:
             # zeros: a page that was never written reads as zeros
             self.pages = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.abi_cache = abi.make_kv4_cache(self.pages, table, k_exp, v_exp)
-        self._plans = {}
+        self._plans, self._row_shapes = {}, set()
 
     @staticmethod
     def exponents(rows) -> torch.Tensor:
@@ -354,9 +360,10 @@ class KV4Cache:
         return torch.clamp(e, -64, 64).to(torch.int32)
 
     # ------------------------------------------------------------- checks
+    # (a condition that holds costs one expression; what is wrong is found and said by the functions)
 
     def _index(self, t, name, n):
-        if t.dtype is not torch.int32 or t.get_device() != self._dev or not t.is_contiguous() or (
+        if t.dtype is not _I32 or t.get_device() != self._dev or not t.is_contiguous() or (
                 n is not None and t.numel() != n):
             raise ValueError(f"{name}: {'' if n is None else n} int32, dense, on {self.device}: "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -367,11 +374,15 @@ class KV4Cache:
             raise ValueError(f"{name}: {self.dtype} {tuple(shape)}{', dense,' if dense else ''} on {self.device}: "
                              f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
+    def _row_shape(self, shape):
+        """Takes [B, T, Hkv, dh] in among the shapes that rows may have."""
+        if len(shape) != 4 or shape[0] != self.batch or shape[1] < 1 or tuple(shape[2:]) != (self.kv_heads, self.head_dim):
+            raise ValueError(f"rows are [{self.batch}, tokens, {self.kv_heads}, {self.head_dim}], got {tuple(shape)}")
+        self._row_shapes.add(shape)
+
     def _stride(self, t, name):
         """Elements between a sequence's consecutive tokens (0: dense); heads
         and values are dense and sequences follow at the same stride."""
-        if t.is_contiguous():
-            return 0
         B, T, H, D = t.shape
         s = t.stride()
         token = s[1] if T > 1 else s[0] if B > 1 else H * D
@@ -383,8 +394,8 @@ class KV4Cache:
         """(the stream's handle, what makes the cache's device and the stream
         current, or None where they are)."""
         if stream is None:
-            return (torch._C._cuda_getCurrentRawStream(self._dev),
-                    None if torch.cuda.current_device() == self._dev else torch.cuda.device(self._dev))
+            return (_current_stream(self._dev),
+                    None if _current_device() == self._dev else torch.cuda.device(self._dev))
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
         if stream.device != self.device:
@@ -396,14 +407,23 @@ class KV4Cache:
     def write(self, K, V, pos, count=None, stream=None):
         """Quantise rows K, V [B, T, Hkv, dh] into positions pos[b] .. of each
         sequence (count[b] of them, or all T).  Rows may be slices of wider
-        ones (a fused projection's)."""
-        shape = (self.batch, K.shape[1], self.kv_heads, self.head_dim)
-        self._rows(K, "K", shape, False)
-        self._rows(V, "V", shape, False)
-        ks, vs = self._stride(K, "K"), self._stride(V, "V")
-        self._index(pos, "pos", self.batch)
-        if count is not None:
-            self._index(count, "count", self.batch)
+        ones (a fused projection's).  Calls that write tokens of the same 16 of
+        a sequence (positions 16 j .. 16 j + 15) must be ordered."""
+        shape, dtype, dev = K.shape, self.dtype, self._dev
+        if shape not in self._row_shapes:
+            self._row_shape(shape)
+        if K.dtype is not dtype or K.get_device() != dev:
+            self._rows(K, "K", shape, False)
+        if V.dtype is not dtype or V.get_device() != dev or V.shape != shape:
+            self._rows(V, "V", shape, False)
+        n = self.batch
+        if pos.dtype is not _I32 or pos.get_device() != dev or pos.numel() != n or not pos.is_contiguous():
+            self._index(pos, "pos", n)
+        if count is not None and (count.dtype is not _I32 or count.get_device() != dev or count.numel() != n
+                                  or not count.is_contiguous()):
+            self._index(count, "count", n)
+        ks = 0 if K.is_contiguous() else self._stride(K, "K")
+        vs = 0 if V.is_contiguous() else self._stride(V, "V")
         handle, within = self._on(stream)
         if within is None:
             abi.sambay_kv4_write(self.abi_cache, self.dims, shape[1], K, V, pos, count, ks, vs, handle)
@@ -415,13 +435,25 @@ class KV4Cache:
         """The rows K, V [B, tokens, Hkv, dh] that positions pos[b] .. stand
         for (count[b] of them, or all); rows from count[b] on are left as they
         were (zeros in tensors made here)."""
-        shape = (self.batch, tokens, self.kv_heads, self.head_dim)
-        self._index(pos, "pos", self.batch)
-        if count is not None:
-            self._index(count, "count", self.batch)
-        if K is not None:
+        n, dtype, dev = self.batch, self.dtype, self._dev
+        if pos.dtype is not _I32 or pos.get_device() != dev or pos.numel() != n or not pos.is_contiguous():
+            self._index(pos, "pos", n)
+        if count is not None and (count.dtype is not _I32 or count.get_device() != dev or count.numel() != n
+                                  or not count.is_contiguous()):
+            self._index(count, "count", n)
+        if K is None or V is None:
+            shape = torch.Size((self.batch, tokens, self.kv_heads, self.head_dim))
+        else:
+            shape = K.shape
+            if shape[1] != tokens:
+                raise ValueError(f"K has {shape[1]} tokens a sequence, not {tokens}")
+        if shape not in self._row_shapes:
+            self._row_shape(shape)
+        if K is not None and (K.dtype is not dtype or K.get_device() != dev or not K.is_contiguous()
+                              or K.shape != shape):
             self._rows(K, "K", shape)
-        if V is not None:
+        if V is not None and (V.dtype is not dtype or V.get_device() != dev or not V.is_contiguous()
+                              or V.shape != shape):
             self._rows(V, "V", shape)
         handle, within = self._on(stream)
         if within is None:
@@ -440,16 +472,21 @@ class KV4Cache:
         of each sequence's lens[b] cached tokens; q [B, Hq, dh] for one token
         a sequence.  Rows from count[b] on are left as they were (zeros in a
         tensor made here)."""
-        shape = q.shape
+        shape, dtype, dev = q.shape, self.dtype, self._dev
         plan = self._plans.get(shape)
         if plan is None:
             plan = self._plan(shape)
-        self._rows(q, "q", shape)
-        if out is not None:
+        if q.dtype is not dtype or q.get_device() != dev or not q.is_contiguous():
+            self._rows(q, "q", shape)
+        if out is not None and (out.dtype is not dtype or out.get_device() != dev or not out.is_contiguous()
+                                or out.shape != shape):
             self._rows(out, "out", shape)
-        self._index(lens, "lens", self.batch)
-        if count is not None:
-            self._index(count, "count", self.batch)
+        n = self.batch
+        if lens.dtype is not _I32 or lens.get_device() != dev or lens.numel() != n or not lens.is_contiguous():
+            self._index(lens, "lens", n)
+        if count is not None and (count.dtype is not _I32 or count.get_device() != dev or count.numel() != n
+                                  or not count.is_contiguous()):
+            self._index(count, "count", n)
         handle, within = self._on(stream)
         if within is None:
             return self._attend(plan, q, lens, count, scale, out, handle)
