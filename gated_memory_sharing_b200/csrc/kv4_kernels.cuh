@@ -901,15 +901,14 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
           raw[n][ks].zero();
     }
   };
-  // where registers allow: on their way while the first pages are looked up
-  constexpr bool kEarly = NT == 1 && !SPLIT;
-  if (kEarly) fetch();
-  issue(0);
-
   uint32_t qb[NQ][NT][KS][2];
   float f[NT][2];
   int lim[NT][2];
   float ref[NT][2], l[NT][2], o[NT][KS][4];
+  // where registers allow, the first queries are on their way while the first pages are looked up
+  constexpr bool kEarly = !SPLIT;
+  if (kEarly) fetch();
+  issue(0);
   bool fresh = true;
   int st = 0, lim_min = 0;
   uint32_t parity = 0;
@@ -980,15 +979,117 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
 
     const uint32_t mask = have >> (SG * st) & ((1u << SG) - 1);
     const uint8_t* stage = ring + st * kStageBytes;
-    // One tile.  EDGE: not every column sees all of its tokens, or some are missing.
-    auto tile = [&](int tok0, const uint8_t* base, uint32_t here, auto edge) {
-      constexpr bool EDGE = decltype(edge)::value;
-      // The tile's scales, 8 of K (`first` kKs) or V (kVs) converted a lane: every
-      // lane needs 1/4 (K) or 1/8 (V) of them, which they would convert 8 and 4 times over.
-      bool nan = false;                // at an edge: one of those staged last (of any token) is NaN
+    // The parts of a tile's work.  S^T of a group (entries 0, 1: token g, columns
+    // 2t, 2t + 1; entries 2, 3: token g + 8); sl: the scales of tokens g and
+    // g + 8, two blocks each.
+    auto scores = [&](float (&s)[NT][4], const uint8_t* grp, const uint32_t (&sl)[2][KS / 2]) {
+#pragma unroll
+      for (int k = 0; k < KS / 4; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kK + k * 512 + lane * 16);
+        const uint32_t kc[2][2] = {{v.x, v.z}, {v.y, v.w}};      // [two blocks][token g, g + 8]
+#pragma unroll
+        for (int bp = 0; bp < 2; ++bp) {               // blocks 4k + 2 bp, + 1
+          uint32_t x0[4], x1[4];
+          e2m1x8_f16x2(kc[bp][0], x0);
+          e2m1x8_f16x2(kc[bp][1], x1);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int kb = 4 * k + 2 * bp + e;
+            const uint32_t s0 = sl[0][2 * k + bp], s1 = sl[1][2 * k + bp];
+            const uint32_t a0 = mul_f16x2_half(x0[2 * e], s0, e), a1 = mul_f16x2_half(x1[2 * e], s1, e);
+            const uint32_t a2 = mul_f16x2_half(x0[2 * e + 1], s0, e), a3 = mul_f16x2_half(x1[2 * e + 1], s1, e);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (kb == 0)
+                mma16816_f16_zero(s[n], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
+              else
+                mma16816_f16(s[n], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
+              if (SPLIT) mma16816_f16(s[n], a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
+            }
+          }
+        }
+      }
+    };
+    // Online softmax per column: p = 2^(f s + ref), f > 0, ref = kPShift less the
+    // largest logit so far; mx: a lane's largest s.  Most tiles hold no larger one.
+    auto raise = [&](const float (&mx)[NT][2]) {
+      bool grown = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) grown |= fmaf(mx[n][e], f[n][e], ref[n][e]) > kPShift;
+      if (!__any_sync(0xFFFFFFFFu, grown)) return;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float corr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = mx[n][e];
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+          const float to = fminf(ref[n][e], kPShift - x * f[n][e]);
+          corr[e] = ex2_approx(to - ref[n][e]);            // 0 from kNoRef
+          ref[n][e] = to;
+          l[n][e] *= corr[e];
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const float2 u = mul2(make_float2(o[n][k][0], o[n][k][1]), make_float2(corr[0], corr[1]));
+          const float2 v = mul2(make_float2(o[n][k][2], o[n][k][3]), make_float2(corr[0], corr[1]));
+          o[n][k][0] = u.x; o[n][k][1] = u.y; o[n][k][2] = v.x; o[n][k][3] = v.y;
+        }
+      }
+    };
+    // P of a group as B fragments, and into the rows' sums.
+    auto probabilities = [&](const float (&s)[NT][4], uint32_t (&pb)[NQ][NT][2]) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float2 fn = make_float2(f[n][0], f[n][1]), rn = make_float2(ref[n][0], ref[n][1]);
+        const float2 u = fma2(make_float2(s[n][0], s[n][1]), fn, rn), v = fma2(make_float2(s[n][2], s[n][3]), fn, rn);
+        const float2 pu = make_float2(ex2_approx(u.x), ex2_approx(u.y)), pv = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+        const float2 ln = add2(make_float2(l[n][0], l[n][1]), add2(pu, pv));
+        l[n][0] = ln.x;
+        l[n][1] = ln.y;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 pe = e ? pv : pu;
+          const uint32_t hi = pack_f16(pe.x, pe.y);
+          pb[0][n][e] = movmatrix_trans(hi);
+          if (SPLIT) {
+            const float2 h2 = f16x2_f32(hi);
+            pb[NQ - 1][n][e] = movmatrix_trans(pack_f16(pe.x - h2.x, pe.y - h2.y));
+          }
+        }
+      }
+    };
+    // O^T += V^T P^T of blocks 4k .. 4k + 3 of a group; lo, hi: the scales of its
+    // tokens 2t, 2t + 1 and 2t + 8, 2t + 9.
+    auto outputs = [&](int k, const uint8_t* grp, const uint32_t (&lo)[4], const uint32_t (&hi)[4],
+                       const uint32_t (&pb)[NQ][NT][2]) {
+      const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kV + k * 512 + lane * 16);
+      uint32_t x0[4], x1[4], x2[4], x3[4];
+      e2m1x8_f16x2(v.x, x0);           // values 2g, tokens 2t, 2t + 1
+      e2m1x8_f16x2(v.y, x1);           // values 2g + 1
+      e2m1x8_f16x2(v.z, x2);           // values 2g, tokens 2t + 8, 2t + 9
+      e2m1x8_f16x2(v.w, x3);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a0 = mul_f16x2(x0[e], lo[e]), a1 = mul_f16x2(x1[e], lo[e]);
+        const uint32_t a2 = mul_f16x2(x2[e], hi[e]), a3 = mul_f16x2(x3[e], hi[e]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
+          if (SPLIT) mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[NQ - 1][n][0], pb[NQ - 1][n][1]);
+        }
+      }
+    };
+    // A tile that every column sees all of.
+    auto whole_tile = [&](const uint8_t* base) {
+      // Its scales, 8 of K or V (`first`) converted a lane: every lane needs 1/4
+      // (K) or 1/8 (V) of them, which they would convert 8 and 4 times over.
       auto stage_scales = [&](int first) {
         const uint2 v = *reinterpret_cast<const uint2*>(base + lane * 8 / D * Block<D>::kBytes + first + lane * 8 % D);
-        if (EDGE) nan = __any_sync(0xFFFFFFFFu, (__vcmpeq4(v.x, 0x7F7F7F7Fu) | __vcmpeq4(v.y, 0x7F7F7F7Fu)) != 0);
         uint4 h;
         e4m3x4_f16x2(v.x, h.x, h.y);
         e4m3x4_f16x2(v.y, h.z, h.w);
@@ -997,172 +1098,119 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
         __syncwarp();
       };
       stage_scales(Block<D>::kKs);
-      // S^T of group q: entries 0, 1: token g, columns 2t, 2t + 1; entries 2, 3: token g + 8
-      float s[NT][GP][4];
+      float s[GP][NT][4], mx[NT][2];
 #pragma unroll
       for (int q = 0; q < GP; ++q) {
-        const uint8_t* grp = base + q * Block<D>::kBytes;
-        if (!EDGE || (here >> q & 1)) {
-          uint32_t kc[KS], sl[2][KS / 2];              // sl: tokens g and g + 8, two blocks each
+        uint32_t sl[2][KS / 2];
 #pragma unroll
-          for (int k = 0; k < KS / 4; ++k) {
-            const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kK + k * 512 + lane * 16);
-            kc[4 * k] = v.x; kc[4 * k + 1] = v.y; kc[4 * k + 2] = v.z; kc[4 * k + 3] = v.w;
-            const uint4 u = *reinterpret_cast<const uint4*>(scales + (q * D + g * (2 * KS)) * 2 + k * 16);
-            if (KS == 4) {
-              sl[0][0] = u.x; sl[0][1] = u.y; sl[1][0] = u.z; sl[1][1] = u.w;
-            } else {
-              sl[k][0] = u.x; sl[k][1] = u.y; sl[k][KS / 2 - 2] = u.z; sl[k][KS / 2 - 1] = u.w;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < KS / 4; ++k) {
-#pragma unroll
-            for (int bp = 0; bp < 2; ++bp) {           // blocks 4k + 2 bp, + 1
-              uint32_t x0[4], x1[4];                   // tokens g and g + 8
-              e2m1x8_f16x2(kc[4 * k + bp], x0);
-              e2m1x8_f16x2(kc[4 * k + 2 + bp], x1);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t a0 = mul_f16x2_half(x0[2 * e], sl[0][2 * k + bp], e), a1 = mul_f16x2_half(x1[2 * e], sl[1][2 * k + bp], e);
-                const uint32_t a2 = mul_f16x2_half(x0[2 * e + 1], sl[0][2 * k + bp], e), a3 = mul_f16x2_half(x1[2 * e + 1], sl[1][2 * k + bp], e);
-                const int kb = 4 * k + 2 * bp + e;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  if (kb == 0)
-                    mma16816_f16_zero(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
-                  else
-                    mma16816_f16(s[n][q], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
-                  if (SPLIT) mma16816_f16(s[n][q], a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
-                }
-              }
-            }
+        for (int k = 0; k < KS / 4; ++k) {
+          const uint4 u = *reinterpret_cast<const uint4*>(scales + (q * D + g * (2 * KS)) * 2 + k * 16);
+          if (KS == 4) {
+            sl[0][0] = u.x; sl[0][1] = u.y; sl[1][0] = u.z; sl[1][1] = u.w;
+          } else {
+            sl[k][0] = u.x; sl[k][1] = u.y; sl[k][KS / 2 - 2] = u.z; sl[k][KS / 2 - 1] = u.w;
           }
         }
-        if (EDGE) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!(here >> q & 1) || tok0 + q * kGroup + g + 8 * (e >> 1) >= lim[n][e & 1]) s[n][q][e] = -INFINITY;
-        }
+        scores(s[q], base + q * Block<D>::kBytes, sl);
       }
-      // online softmax per column: p = 2^(f s + ref), f > 0, ref = kPShift less the
-      // largest logit so far; most tiles hold no larger one
-      bool grown = false;
-      float mx[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[n][e] = fmaxf(s[n][0][e], s[n][0][e + 2]);
+          mx[n][e] = fmaxf(s[0][n][e], s[0][n][e + 2]);
 #pragma unroll
-          for (int q = 1; q < GP; ++q) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[n][q][e], s[n][q][e + 2]));
-          grown |= fmaf(mx[n][e], f[n][e], ref[n][e]) > kPShift;
+          for (int q = 1; q < GP; ++q) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[q][n][e], s[q][n][e + 2]));
         }
-      if (__any_sync(0xFFFFFFFFu, grown)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float corr[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = mx[n][e];
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-            const float to = fminf(ref[n][e], kPShift - x * f[n][e]);
-            corr[e] = ex2_approx(to - ref[n][e]);          // 0 from kNoRef
-            ref[n][e] = to;
-            l[n][e] *= corr[e];
-          }
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const float2 u = mul2(make_float2(o[n][k][0], o[n][k][1]), make_float2(corr[0], corr[1]));
-            const float2 v = mul2(make_float2(o[n][k][2], o[n][k][3]), make_float2(corr[0], corr[1]));
-            o[n][k][0] = u.x; o[n][k][1] = u.y; o[n][k][2] = v.x; o[n][k][3] = v.y;
-          }
-        }
-      }
+      raise(mx);
       stage_scales(Block<D>::kVs);
 #pragma unroll
       for (int q = 0; q < GP; ++q) {
-        if (EDGE && !(here >> q & 1)) continue;
-        const uint8_t* grp = base + q * Block<D>::kBytes;
-        const int tok = tok0 + q * kGroup;
         uint32_t pb[NQ][NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 fn = make_float2(f[n][0], f[n][1]), rn = make_float2(ref[n][0], ref[n][1]);
-          const float2 u = fma2(make_float2(s[n][q][0], s[n][q][1]), fn, rn);
-          const float2 v = fma2(make_float2(s[n][q][2], s[n][q][3]), fn, rn);
-          const float2 pu = make_float2(ex2_approx(u.x), ex2_approx(u.y)), pv = make_float2(ex2_approx(v.x), ex2_approx(v.y));
-          const float2 ln = add2(make_float2(l[n][0], l[n][1]), add2(pu, pv));
-          l[n][0] = ln.x;
-          l[n][1] = ln.y;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 pe = e ? pv : pu;
-            const uint32_t hi = pack_f16(pe.x, pe.y);
-            pb[0][n][e] = movmatrix_trans(hi);
-            if (SPLIT) {
-              const float2 h2 = f16x2_f32(hi);
-              pb[NQ - 1][n][e] = movmatrix_trans(pack_f16(pe.x - h2.x, pe.y - h2.y));
-            }
-          }
-        }
-        // O^T += V^T P^T.  At an edge the scales of tokens that are not the
-        // sequence's are blanked, whose P is 0 (0 x NaN is not), and a block of
-        // NaN reaches only the columns that see its token: its scale is blanked
-        // too, and these columns are set to NaN.
-        uint32_t keep_lo = 0, keep_hi = 0;           // halves of the sequence's own tokens 2t, 2t + 1 and 2t + 8, 2t + 9
-        if (EDGE) {
-          const int left = c.len - tok - 2 * t;
-          keep_lo = left > 1 ? 0xFFFFFFFFu : left > 0 ? 0xFFFFu : 0u;
-          keep_hi = left > 9 ? 0xFFFFFFFFu : left > 8 ? 0xFFFFu : 0u;
-        }
+        probabilities(s[q], pb);
 #pragma unroll
         for (int k = 0; k < KS / 4; ++k) {
-          const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kV + k * 512 + lane * 16);
           const uint4* sv = reinterpret_cast<const uint4*>(scales + (q * D + t * (4 * KS) + k * 16) * 2);
-          const uint4 s01 = sv[0], s23 = sv[1];
-          uint32_t lo[4] = {s01.x, s01.z, s23.x, s23.z}, hi[4] = {s01.y, s01.w, s23.y, s23.w};
-          uint32_t x0[4], x1[4], x2[4], x3[4];
-          e2m1x8_f16x2(v.x, x0);       // values 2g, tokens 2t, 2t + 1
-          e2m1x8_f16x2(v.y, x1);       // values 2g + 1
-          e2m1x8_f16x2(v.z, x2);       // values 2g, tokens 2t + 8, 2t + 9
-          e2m1x8_f16x2(v.w, x3);
+          const uint4 u = sv[0], v = sv[1];
+          const uint32_t lo[4] = {u.x, u.z, v.x, v.z}, hi[4] = {u.y, u.w, v.y, v.w};
+          outputs(k, base + q * Block<D>::kBytes, lo, hi, pb);
+        }
+      }
+    };
+    // A group of a tile that columns see different parts of, or that is not all
+    // there.  Few tiles are: short code, a group at a time, counts for more than
+    // its speed (twice the code here cost calls of 12 to 33 us 3.5 us each).
+    auto edge_group = [&](int tok, const uint8_t* grp) {
+      uint32_t sl[2][KS / 2];
+      if (KS == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(grp + Block<D>::kKs + g * 8);
+        e4m3x4_f16x2(u.x, sl[0][0], sl[0][1]);
+        e4m3x4_f16x2(u.y, sl[1][0], sl[1][1]);
+      } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(grp + Block<D>::kKs + g * 16);
+        e4m3x4_f16x2(u.x, sl[0][0], sl[0][1]);
+        e4m3x4_f16x2(u.y, sl[0][KS / 2 - 2], sl[0][KS / 2 - 1]);
+        e4m3x4_f16x2(u.z, sl[1][0], sl[1][1]);
+        e4m3x4_f16x2(u.w, sl[1][KS / 2 - 2], sl[1][KS / 2 - 1]);
+      }
+      float s[NT][4], mx[NT][2];
+      scores(s, grp, sl);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (tok + g >= lim[n][e]) s[n][e] = -INFINITY;
+          if (tok + g + 8 >= lim[n][e]) s[n][e + 2] = -INFINITY;
+          mx[n][e] = fmaxf(s[n][e], s[n][e + 2]);
+        }
+      raise(mx);
+      uint32_t pb[NQ][NT][2];
+      probabilities(s, pb);
+      // The scales of tokens that are not the sequence's are blanked, whose P is 0
+      // (0 x NaN is not).  A block of NaN reaches only the columns that see its
+      // token: its scale is blanked too, and these columns are set to NaN after.
+      uint32_t keep = 0, w[KS], nan = 0, bad[KS / 4];    // bad: per block the first such token of the group, a byte each
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (tok + 2 * t + (e & 1) + 8 * (e >> 1) < c.len) keep |= 0xFFu << (8 * e);
+#pragma unroll
+      for (int k = 0; k < KS / 4; ++k) {
+        const uint4 u = *reinterpret_cast<const uint4*>(grp + Block<D>::kVs + t * (4 * KS) + 16 * k);
+        w[4 * k] = u.x & keep; w[4 * k + 1] = u.y & keep; w[4 * k + 2] = u.z & keep; w[4 * k + 3] = u.w & keep;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) nan |= __vcmpeq4(w[4 * k + e], 0x7F7F7F7Fu);
+      }
+      const bool any_nan = __any_sync(0xFFFFFFFFu, nan != 0);
+      if (any_nan) {
+#pragma unroll
+        for (int k = 0; k < KS / 4; ++k) {
+          bad[k] = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            int bad = 0x7FFFFFFF;                     // first token of the group whose block is NaN
-            if (EDGE) {
-              lo[e] &= keep_lo;
-              hi[e] &= keep_hi;
-            }
-            if (EDGE && nan) {
-              // a scale's f16 is at most 0x5F00, a NaN's over 0x7C00
-              const uint32_t nan_lo = __vcmpgtu2(lo[e] & 0x7FFF7FFFu, 0x7C007C00u), nan_hi = __vcmpgtu2(hi[e] & 0x7FFF7FFFu, 0x7C007C00u);
-              if (__any_sync(0xFFFFFFFFu, (nan_lo | nan_hi) != 0)) {
-                lo[e] &= ~nan_lo;
-                hi[e] &= ~nan_hi;
-                if (nan_lo | nan_hi)
-                  bad = tok + 2 * t + (nan_lo & 0xFFFFu ? 0 : nan_lo ? 1 : nan_hi & 0xFFFFu ? 8 : 9);
-                bad = min(bad, __shfl_xor_sync(0xFFFFFFFFu, bad, 1));
-                bad = min(bad, __shfl_xor_sync(0xFFFFFFFFu, bad, 2));
-              }
-            }
-            const uint32_t a0 = mul_f16x2(x0[e], lo[e]), a1 = mul_f16x2(x1[e], lo[e]);
-            const uint32_t a2 = mul_f16x2(x2[e], hi[e]), a3 = mul_f16x2(x3[e], hi[e]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
-              if (SPLIT) mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[NQ - 1][n][0], pb[NQ - 1][n][1]);
-              if (EDGE && nan) {
-#pragma unroll
-                for (int i2 = 0; i2 < 4; ++i2)
-                  if (bad < lim[n][i2 & 1]) o[n][4 * k + e][i2] = __int_as_float(0x7FC00000);
-              }
-            }
+            const uint32_t is = __vcmpeq4(w[4 * k + e], 0x7F7F7F7Fu);
+            w[4 * k + e] &= ~is;
+            const int first = is & 0xFFu ? 2 * t : is & 0xFF00u ? 2 * t + 1 : is & 0xFF0000u ? 2 * t + 8 : is ? 2 * t + 9 : 0xFF;
+            bad[k] |= static_cast<uint32_t>(first) << (8 * e);
           }
+          bad[k] = __vminu4(bad[k], __shfl_xor_sync(0xFFFFFFFFu, bad[k], 1));
+          bad[k] = __vminu4(bad[k], __shfl_xor_sync(0xFFFFFFFFu, bad[k], 2));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < KS / 4; ++k) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) e4m3x4_f16x2(w[4 * k + e], lo[e], hi[e]);
+        outputs(k, grp, lo, hi, pb);
+      }
+      if (any_nan) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int first = bad[k / 4] >> (8 * (k % 4)) & 0xFF;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (first < 16 && tok + first < lim[n][e & 1]) o[n][k][e] = __int_as_float(0x7FC00000);
         }
       }
     };
@@ -1170,10 +1218,13 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
     for (int k = 0; k < n; ++k) {
       const int tok0 = (c.tile + k) * TILE;
       const uint32_t here = mask >> (GP * k) & ((1u << GP) - 1);
-      if (here == (1u << GP) - 1 && tok0 + TILE <= lim_min)
-        tile(tok0, stage + k * kTileBytes, here, std::false_type());
-      else
-        tile(tok0, stage + k * kTileBytes, here, std::true_type());
+      if (here == (1u << GP) - 1 && tok0 + TILE <= lim_min) {
+        whole_tile(stage + k * kTileBytes);
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < GP; ++q)
+          if (here >> q & 1) edge_group(tok0 + q * kGroup, stage + k * kTileBytes + q * Block<D>::kBytes);
+      }
     }
     __syncwarp();                      // the stage is read; the next iteration's copies may refill it
     st ^= 1;

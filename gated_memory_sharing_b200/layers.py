@@ -386,7 +386,7 @@ class KV4Cache:
         B, T, H, D = t.shape
         s = t.stride()
         token = s[1] if T > 1 else s[0] if B > 1 else H * D
-        if s[3] != 1 or (H > 1 and s[2] != D) or (B > 1 and s[0] != T * token):
+        if s[3] != 1 or (H > 1 and s[2] != D) or (B > 1 and s[0] != T * token) or token < H * D:
             raise ValueError(f"{name}: strides {s} are not [tokens * stride, stride, {D}, 1]")
         return token
 

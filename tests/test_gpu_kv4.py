@@ -235,6 +235,31 @@ def test_attention_of_several_tokens(T, Hq, Hkv, dh, lens, count, dtype):
         assert torch.all(out[b, n:] == 7.0)                                       # rows that are none: left as they were
 
 
+@pytest.mark.parametrize("dtype,Hq,Hkv,dh,page", [(BF16, 16, 8, 64, 32), (F32, 8, 8, 128, 16), (BF16, 128, 8, 64, 128)])
+def test_many_long_and_short_sequences(dtype, Hq, Hkv, dh, page):
+    """Warps' shares that are long (where changing to another sequence counts in
+    them), with runs of empty and short sequences; some sequences against the oracle."""
+    lens = [3000 - i if i % 9 == 0 else (0, 1, 64, 700, 65, 2000, 0, 5)[i % 8] for i in range(120)]
+    B = len(lens)
+    assert Hkv * sum(max(1, -(-n * dh // 4096)) for n in lens) >= 4 * 148 * 3 * 4
+    K, V = rows(55, B, max(lens), Hkv, dh, dtype=dtype), rows(56, B, max(lens), Hkv, dh, dtype=dtype)
+    c = make(B, Hkv, dh, max(lens), page, dtype)
+    c.write(K, V, i32([0] * B), i32(lens))
+    q = rows(57, B, 1, Hq, dh, dtype=dtype)
+    out = c.attend(q, i32(lens))
+    some = [0, 1, 3, 5, 8, 9, 40, 63, 90, 112, 117, 119]
+    at = torch.tensor(some, device="cuda")
+    check(out[at], q[at], kv4_kept(f64(K[at])), kv4_kept(f64(V[at])), [lens[i] for i in some], what="long and short")
+    assert torch.isfinite(out).all() and torch.all(out[i32([i for i in range(B) if lens[i] == 0]).long()] == 0)
+    assert torch.equal(out, c.attend(q, i32(lens)))
+    # a sequence alone: other shares, the same bound
+    kk, vv = kv4_kept(f64(K[at])), kv4_kept(f64(V[at]))
+    for j in (0, 2, 8):
+        one = i32([lens[some[j]] if i == some[j] else 0 for i in range(B)])
+        alone = c.attend(q, one)
+        check(alone[at][j:j + 1], q[at][j:j + 1], kk[j:j + 1], vv[j:j + 1], [lens[some[j]]], what="alone")
+
+
 def test_exponents_and_scale():
     B, H, dh, lens = 2, 4, 64, [130, 77]
     Kr, Vr = rows(60, B, 130, H, dh, scale=2.0 ** -20), rows(61, B, 130, H, dh, scale=2.0 ** 13)
@@ -429,6 +454,38 @@ def test_streams_and_graphs():
         assert same(f64(c.read(pos, 1)[0]), kv4_kept(f64(x)))
 
 
+def test_after_other_work_in_a_graph():
+    """Captured behind a copy, a fill, and a join with another stream: each call still follows what was queued before it."""
+    lens = [200, 77]
+    c, _, _ = filled(2, 4, 64, 16, lens, BF16, seed=190)
+    n = i32(lens)
+    src, q, x, xs = rows(191, 2, 1, 8, 64), rows(192, 2, 1, 8, 64), rows(193, 2, 1, 4, 64), rows(194, 2, 1, 4, 64)
+    wants = []
+    for k in range(3):
+        src.copy_(rows(195 + k, 2, 1, 8, 64))
+        xs.copy_(rows(198 + k, 2, 1, 4, 64))
+        c.write(xs, xs, i32([199, 76]))
+        wants.append(c.attend(src, n))
+    side, out = torch.cuda.Stream(), torch.empty_like(q)
+    pos = i32([199, 76])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.copy_(src)
+        out.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            x.copy_(xs)
+        torch.cuda.current_stream().wait_stream(side)
+        c.write(x, x, pos)
+        c.attend(q, n, out=out)
+        Ko, _ = c.read(pos, 1)
+    for k in range(3):
+        src.copy_(rows(195 + k, 2, 1, 8, 64))
+        xs.copy_(rows(198 + k, 2, 1, 4, 64))
+        g.replay()
+        assert torch.equal(out, wants[k]) and same(f64(Ko), kv4_kept(f64(xs)))
+
+
 def test_layer_refusals():
     c = KV4Cache(2, 4, 64, 100, page_tokens=16)
     k = rows(180, 2, 5, 4, 64)
@@ -438,6 +495,8 @@ def test_layer_refusals():
                 lambda: c.write(k, k, pos.long()), lambda: c.write(k, k, pos.cpu()), lambda: c.write(k, k, i32([0])),
                 lambda: c.write(k.cpu(), k, pos), lambda: c.write(k, k, pos, i32([1, 2, 3])),
                 lambda: c.write(rows(181, 2, 10, 4, 64)[:, ::2].expand(2, 5, 4, 64)[:, :, :, :32], k, pos),
+                lambda: c.write(k[:, :1].expand(2, 5, 4, 64), k, pos), lambda: c.write(k, k[:1].expand(2, 5, 4, 64), pos),
+                lambda: c.write(k[:, :0], k[:, :0], pos), lambda: c.read(pos, 0), lambda: c.attend(k[:, :0], pos),
                 lambda: c.read(pos, 5, K=k.float()), lambda: c.read(pos, 4, K=k), lambda: c.read(pos.float(), 4),
                 lambda: c.attend(k, pos.long()), lambda: c.attend(k.float(), pos), lambda: c.attend(k, pos, out=k[:, :2]),
                 lambda: c.attend(k.transpose(0, 1), pos), lambda: c.attend(k[:, :, :, :32], pos)):
