@@ -495,7 +495,7 @@ class KV4Cache:
 
     def _plan(self, shape):
         """(query heads, tokens, workspace bytes) for queries of this shape."""
-        if len(shape) not in (3, 4) or shape[0] != self.batch or shape[-1] != self.head_dim:
+        if len(shape) not in (3, 4) or shape[0] != self.batch or shape[-1] != self.head_dim or 0 in shape:
             raise ValueError(f"q: [{self.batch}, tokens, heads, {self.head_dim}] or without tokens, got {tuple(shape)}")
         heads, tokens = shape[-2], shape[1] if len(shape) == 4 else 1
         plan = heads, tokens, abi.sambay_cross_attn_decode_kv4_workspace(self.dims, heads, tokens)
