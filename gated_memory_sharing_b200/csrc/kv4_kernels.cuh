@@ -983,6 +983,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
     // 2t, 2t + 1; entries 2, 3: token g + 8); sl: the scales of tokens g and
     // g + 8, two blocks each.
     auto scores = [&](float (&s)[NT][4], const uint8_t* grp, const uint32_t (&sl)[2][KS / 2]) {
+      float part[NT][4];
 #pragma unroll
       for (int k = 0; k < KS / 4; ++k) {
         const uint4 v = *reinterpret_cast<const uint4*>(grp + Block<D>::kK + k * 512 + lane * 16);
@@ -1000,11 +1001,28 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
             const uint32_t a2 = mul_f16x2_half(x0[2 * e + 1], s0, e), a3 = mul_f16x2_half(x1[2 * e + 1], s1, e);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              if (kb == 0)
+              if (SPLIT) {
+                // two blocks' products, then added in f32: the tensor cores' own sums
+                // cut what f32 rounds, and over many tokens that shows
+                float (&d)[4] = part[n];
+                if (kb % 2 == 0)
+                  mma16816_f16_zero(d, a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
+                else
+                  mma16816_f16(d, a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
+                mma16816_f16(d, a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
+                if (kb == 1) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) s[n][i] = d[i];
+                } else if (kb % 2 == 1) {
+                  const float2 u = add2(make_float2(s[n][0], s[n][1]), make_float2(d[0], d[1]));
+                  const float2 v = add2(make_float2(s[n][2], s[n][3]), make_float2(d[2], d[3]));
+                  s[n][0] = u.x; s[n][1] = u.y; s[n][2] = v.x; s[n][3] = v.y;
+                }
+              } else if (kb == 0) {
                 mma16816_f16_zero(s[n], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
-              else
+              } else {
                 mma16816_f16(s[n], a0, a1, a2, a3, qb[0][n][kb][0], qb[0][n][kb][1]);
-              if (SPLIT) mma16816_f16(s[n], a0, a1, a2, a3, qb[NQ - 1][n][kb][0], qb[NQ - 1][n][kb][1]);
+              }
             }
           }
         }
@@ -1079,12 +1097,23 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
         const uint32_t a2 = mul_f16x2(x2[e], hi[e]), a3 = mul_f16x2(x3[e], hi[e]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
-          if (SPLIT) mma16816_f16(o[n][4 * k + e], a0, a1, a2, a3, pb[NQ - 1][n][0], pb[NQ - 1][n][1]);
+          float (&acc)[4] = o[n][4 * k + e];
+          if (SPLIT) {
+            float d[4];
+            mma16816_f16_zero(d, a0, a1, a2, a3, pb[NQ - 1][n][0], pb[NQ - 1][n][1]);
+            mma16816_f16(d, a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
+            const float2 u = add2(make_float2(acc[0], acc[1]), make_float2(d[0], d[1]));
+            const float2 v = add2(make_float2(acc[2], acc[3]), make_float2(d[2], d[3]));
+            acc[0] = u.x; acc[1] = u.y; acc[2] = v.x; acc[3] = v.y;
+          } else {
+            mma16816_f16(acc, a0, a1, a2, a3, pb[0][n][0], pb[0][n][1]);
+          }
         }
       }
     };
-    // A tile that every column sees all of.
+    // A tile that every column sees all of.  (f32 at head size 128 would spill
+    // here, and takes all tiles by groups: 16 x 4096 tokens, 128 heads on 8, 48 us, 64 us so.)
+    constexpr bool kWhole = !(SPLIT && D == 128);
     auto whole_tile = [&](const uint8_t* base) {
       // Its scales, 8 of K or V (`first`) converted a lane: every lane needs 1/4
       // (K) or 1/8 (V) of them, which they would convert 8 and 4 times over.
@@ -1218,7 +1247,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
     for (int k = 0; k < n; ++k) {
       const int tok0 = (c.tile + k) * TILE;
       const uint32_t here = mask >> (GP * k) & ((1u << GP) - 1);
-      if (here == (1u << GP) - 1 && tok0 + TILE <= lim_min) {
+      if (kWhole && here == (1u << GP) - 1 && tok0 + TILE <= lim_min) {
         whole_tile(stage + k * kTileBytes);
       } else {
 #pragma unroll 1
