@@ -435,6 +435,9 @@ __device__ __forceinline__ void load_rows(const T* p, long long stride, const in
         x[i][b].zero();
 }
 
+// Bound by the rows' bytes (bf16: 2 in and 0.56 out an element) and by ALU
+// instructions (about 350 of 700 for a unit's 2048 elements).  4 x 32768 bf16
+// tokens of 20 heads of 64: 151 us, 5.7 TB/s, 0.87 of the copy bandwidth.
 // Warp: one unit.  Bytes of the group that belong to other tokens keep their
 // values: K's codes and both scales are stored per token; of V's codes, where
 // two tokens share a byte, a group that is not all the call's is read first.
@@ -516,6 +519,7 @@ __device__ __forceinline__ void store_rows(T* p, long long stride, const int (&r
   }
 }
 
+// Bound by bytes: 4 x 32768 bf16 tokens back in 140 us, 6.1 TB/s, 0.94 of the copy bandwidth.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kRowWarps) kv4_read_kernel(const RowParams<T> p) {
   const Pages& pg = p.pg;
@@ -663,11 +667,11 @@ template <int D>
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + 4096 / D - 1) / (4096 / D)); }
 
 // The line is measured in units, one a tile and, where shares are long, kSwitch
-// more in front of each pair's first: what changing to a pair costs a warp (a
-// batch with empty and short sequences would else leave some warps with many
-// of them: 37 sequences of 0 .. 5000 tokens took 37 us).  Its length (below
-// 2^31, the host sees to it) is cut into shares, none without a tile: share w
-// has `base` units, or one more (the first `rem` of them).
+// more in front of each pair's first: what changing to a pair costs a warp, so
+// that a run of empty and short sequences is not one warp's (37 sequences of 0 ..
+// 5000 tokens: 33.4 us, without it 37.0 us; 1 and 4 units: 34.3 and 33.9 us).
+// The line's length (below 2^31, the host sees to it) is cut into shares, none
+// without a tile: share w has `base` units, or one more (the first `rem`).
 constexpr int kSwitch = 2;
 struct Line {
   int shares, base, rem;
@@ -731,6 +735,11 @@ __device__ __forceinline__ bool advance(const AttnParams& p, Cursor& c, int n) {
   return true;
 }
 
+// Units left of `left` after n tiles; 0 behind the last sequence.
+__device__ __forceinline__ int pair_left(const AttnParams& p, const Cursor& c, int left, int n) {
+  return c.b < p.pg.B ? left - n : 0;
+}
+
 // Inclusive sums over the warp's lanes.
 __device__ __forceinline__ int scan(int v) {
   const int lane = threadIdx.x & 31;
@@ -745,7 +754,9 @@ __device__ __forceinline__ int scan(int v) {
 // The place in the line where share gw begins, and the units from there to its
 // end: 0 where the share is none (one warp).  A lane sums the tiles of B / 32
 // sequences; then the sequences of the lane that holds the place are looked
-// through.  *gap: the line's.
+// through.  *gap: the line's.  (Lengths must not change while a call runs; if
+// they do, what is computed is undefined, but stays inside the arrays: here, in
+// pair_left() and in the combine kernel.)
 template <int D>
 __device__ __forceinline__ int begin_of(const AttnParams& p, int gw, Cursor& c, int* gap) {
   const int lane = threadIdx.x & 31;
@@ -767,7 +778,8 @@ __device__ __forceinline__ int begin_of(const AttnParams& p, int gw, Cursor& c, 
   x -= __shfl_sync(0xFFFFFFFFu, before, k) * pairs;
   c.b = k;
   if (per > 1) {
-    for (int b0 = k * per;; b0 += 32) {              // ends: x is in the line
+    bool found = false;
+    for (int b0 = k * per; b0 < p.pg.B && !found; b0 += 32) {
       const int i = b0 + lane;
       len = i < p.pg.B ? len_of(p, i, false) : 0;
       mine = i < p.pg.B ? tiles_of<D>(len) + line.gap : 0;
@@ -777,15 +789,18 @@ __device__ __forceinline__ int begin_of(const AttnParams& p, int gw, Cursor& c, 
         k = __ffs(past) - 1;
         x -= __shfl_sync(0xFFFFFFFFu, sum - mine, k) * pairs;
         c.b = b0 + k;
-        break;
+        found = true;
+      } else {
+        x -= __shfl_sync(0xFFFFFFFFu, sum, 31) * pairs;
       }
-      x -= __shfl_sync(0xFFFFFFFFu, sum, 31) * pairs;
     }
+    if (!found) return 0;                            // lengths that changed meanwhile
   }
   c.len = __shfl_sync(0xFFFFFFFFu, len, k);
   c.tiles = tiles_of<D>(c.len);
   const int units = c.tiles + line.gap;
   const int pair = static_cast<unsigned>(x) / static_cast<unsigned>(units);
+  if (pair >= pairs) return 0;                       // as above
   x -= pair * units + line.gap;
   c.tile = max(0, x);
   left += min(0, x);                                 // a share that begins in a pair's gap
@@ -800,6 +815,16 @@ __device__ __forceinline__ void prefetch_part(const void* p, long long bytes) {
   if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p) + at));
 }
 
+// Bound by the cache's bytes (4.5 bits an element) and nearly as much by what
+// unpacking them costs: a scheduler dispatches, for 16
+// tokens of 64 values, 32 conversions of codes (2 clocks each), 32 multiplies by
+// scales (1.4), 8 MMAs (3.4) and the softmax, about 190 clocks of the 198 that
+// the bytes take at 6.56 TB/s.  Measured (a captured pass, the combine kernel in
+// it): 16 sequences x 34816 tokens 143 us, 5.6 TB/s, 0.86 of the copy bandwidth
+// (without its loads 133 us, without its arithmetic 125 us); 64 x 2048 43 us,
+// 4.4 TB/s, of which about 13 us are starting (lengths, table, first tiles one
+// after the other), the last parts and the combine kernel.
+//
 // Query row r of a (sequence, KV head): token r / G, head r % G of the group.
 // The MMAs compute S^T = K Q^T and O^T = V^T P^T: tokens (values) are the 16
 // rows of A, straight from the cache's layout, and 8 query rows the columns.
@@ -878,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
       bulk_load(ring_addr + st * kStageBytes + lane * Block<D>::kBytes, src, __popc(piece) * Block<D>::kBytes, bar);
     have = (have & ~(((1u << SG) - 1) << (SG * st))) | mask << (SG * st);
     window = advance<D>(p, in, n);
-    to_load -= window ? n + gap : n;
+    to_load = window ? pair_left(p, in, to_load, n + gap) : to_load - n;
   };
   // The queries of a pair, as they lie there: column g's values 16 b + 4 t .. + 3.
   Four<T> raw[NT][KS];
@@ -1293,7 +1318,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
         }
       fresh = true;
     }
-    left -= advance<D>(p, c, n) ? n + gap : n;
+    left = advance<D>(p, c, n) ? pair_left(p, c, left, n + gap) : left - n;
     i += n;
   }
 }
@@ -1312,7 +1337,8 @@ struct RowSum {
 };
 
 // Rows whose pair was shared by several warps, from their parts in the line's
-// order.  Grid y: sequences.
+// order.  Grid y: sequences.  A few us, nearly all of it latency (its launch
+// overlaps the attention's end, its lengths are read before that).
 //   COLS > 0: a warp for COLS columns of a pair, D / 32 values a lane.
 //   COLS = 0: a CTA for 32 values of a row; 8 lanes take 4 values each, 32 of
 //   them every 32nd part, and then their sums are added in order.
@@ -1335,7 +1361,8 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
   const Line line = line_of<D>(p, b, &before);
   const int tiles = tiles_of<D>(len_of<true>(p, b, false));
   const int a = before + (in ? pair : 0) * (tiles + line.gap);
-  const int w0 = line.share_of(a + line.gap), w1 = line.share_of(a + line.gap + tiles - 1);
+  const int w0 = min(line.shares - 1, line.share_of(a + line.gap));
+  const int w1 = min(line.shares - 1, line.share_of(a + line.gap + tiles - 1));
   const int first = line.begin(w0) >= a ? 0 : 1;       // whether the share begins with this pair
   const int rows = rows_of<true>(p.count, b, p.T_, false) * p.G;       // real ones of a KV head
   const float ve = pow2i(head_exp<true>(pg.v_exp, in ? h : 0));
