@@ -436,7 +436,7 @@ __device__ __forceinline__ void load_rows(const T* p, long long stride, const in
 }
 
 // Bound by the rows' bytes (bf16: 2 in and 0.56 out an element) and by ALU
-// instructions (about 350 of 700 for a unit's 2048 elements).  4 x 32768 bf16
+// instructions (about 330 of 730 for a unit's 2048 elements).  4 x 32768 bf16
 // tokens of 20 heads of 64: 151 us, 5.7 TB/s, 0.87 of the copy bandwidth.
 // Warp: one unit.  Bytes of the group that belong to other tokens keep their
 // values: K's codes and both scales are stored per token; of V's codes, where

@@ -385,7 +385,7 @@ typedef struct {
   int32_t kv_heads;     /* Hkv key/value heads                                */
   int32_t head_dim;     /* dh: 64 or 128                                      */
   int32_t page_tokens;  /* P tokens a page: a power of two, 16 .. 1024        */
-  int32_t num_pages;    /* pages of the pool                                  */
+  int32_t num_pages;    /* pages of the pool (a page is at most 1 GB)         */
   int32_t table_pages;  /* columns of the table: a sequence has room for
                            table_pages * P tokens (at most 2^30)              */
   int32_t io;           /* sambay_dtype of K, V, q and out                    */
@@ -415,17 +415,22 @@ typedef struct {
  * inside a page is the library's own.
  *
  * Sequences may share pages that none of them writes.  The table, pos, count
- * and lens are read on the device, when the call runs; a page outside the pool,
- * a position outside the table or a count outside 0 .. tokens is skipped and
- * recorded (sambay_device_status: SAMBAY_ERR_INVALID_ARG), the rest of the call
- * completes.  int32 arrays are 4-byte aligned.
+ * and lens are read on the device, when the call runs, and must not change while
+ * it does; a page outside the pool, a position outside the table or a count
+ * outside 0 .. tokens is skipped and recorded (sambay_device_status:
+ * SAMBAY_ERR_INVALID_ARG), the rest of the call completes.  int32 arrays are
+ * 4-byte aligned.  The first kernel of these calls is launched programmatically
+ * too: it may be set up while the kernel in front of it finishes, and waits for
+ * it before it reads or writes anything.  batch and Hkv are at most 65535.
  */
 SAMBAY_API size_t sambay_kv4_cache_bytes(const sambay_kv4_dims* dims);
 
 /*
  * sambay_kv4_write - quantise K and V rows into the cache: row t of sequence b
  * goes to position pos[b] + t, t < count[b] (a prompt's rows, or with tokens =
- * 1 a decode step's).  Only the bytes of these positions change.
+ * 1 a decode step's).  What other positions hold stays as it is; calls that
+ * write positions of the same 16 (16 j .. 16 j + 15) of a sequence must be
+ * ordered, since two tokens share a byte.
  *
  *   K, V   [B, tokens, Hkv, dh] io; heads and values dense, consecutive tokens
  *          k_stride / v_stride elements apart (0: Hkv * dh; else at least that,
@@ -461,10 +466,15 @@ SAMBAY_API sambay_status sambay_kv4_read(const sambay_kv4_cache* cache, const sa
  *   for 1 / sqrt(dh).
  *   ws: >= sambay_cross_attn_decode_kv4_workspace(dims, q_heads, tokens); no
  *   initialisation needed, not shared by two calls in flight at once.
+ *   Hkv times the row tiles (of 8 or 16 rows of G * tokens) times the table's
+ *   tiles (of 4096 / dh tokens) times B must stay below 2^31.
  * Products are float32 accumulations of f16 operands: what the cache holds is
  * exact in f16, q is scaled per row by a power of two, and the probabilities
  * are rounded to f16 (SAMBAY_F32: q and the probabilities are split into pairs
- * of f16, 22 bits).
+ * of f16, 22 bits).  A value that is NaN reaches only the queries that see its
+ * token.  Results do not vary from run to run (parts are joined in a fixed
+ * order); how the work is cut depends on all sequences' lengths, so a sequence's
+ * last bits may differ with the batch it is in.
  */
 SAMBAY_API size_t sambay_cross_attn_decode_kv4_workspace(const sambay_kv4_dims* dims, int32_t q_heads,
                                                          int32_t tokens);
