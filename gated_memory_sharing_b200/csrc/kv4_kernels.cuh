@@ -1339,10 +1339,11 @@ struct RowSum {
 // Rows whose pair was shared by several warps, from their parts in the line's
 // order.  Grid y: sequences.  A few us, nearly all of it latency (its launch
 // overlaps the attention's end, its lengths are read before that).
-//   COLS > 0: a warp for COLS columns of a pair, D / 32 values a lane.
+//   COLS > 0: WARPS warps (each every WARPS-th part) for COLS columns of a pair,
+//   D / 32 values a lane.
 //   COLS = 0: a CTA for 32 values of a row; 8 lanes take 4 values each, 32 of
 //   them every 32nd part, and then their sums are added in order.
-template <typename T, int D, int NT, int COLS>
+template <typename T, int D, int NT, int COLS, int WARPS = 1>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
   constexpr bool MANY = COLS == 0;
   constexpr int kCols = MANY ? 1 : COLS;
@@ -1351,7 +1352,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y;
   // the pair, its first column here, and the lane's first value
-  const unsigned u = MANY ? blockIdx.x / SLICES : blockIdx.x * 8 + warp;
+  const unsigned u = MANY ? blockIdx.x / SLICES : blockIdx.x * (8 / WARPS) + warp / WARPS;
   const unsigned per = (p.cols + kCols - 1) / kCols;
   const int pair = u / per, col0 = (u - pair * per) * kCols;
   const int at = MANY ? blockIdx.x % SLICES * 32 + (threadIdx.x & 7) * 4 : lane * V;
@@ -1382,7 +1383,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
   if (!MANY) {
     RowSum<V> sum[kCols];
 #pragma unroll kCols == 1 ? 4 : 2
-    for (int w = w0; w <= w1; ++w) {
+    for (int w = w0 + warp % WARPS; w <= w1; w += WARPS) {
       const long long k = (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col0;
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
@@ -1393,6 +1394,26 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
           for (int v = 0; v < V; v += 2) load2(p.o_part + (k + c) * D + at + v, x + v);
           sum[c].add(ml.x, ml.y, x);
         }
+    }
+    if constexpr (WARPS > 1) {
+      static_assert(WARPS == 1 || COLS == 1, "several warps take one row");
+      __shared__ float part[8][32][V + 2];
+      float* mine = part[warp][lane];
+      mine[V] = sum[0].m;
+      mine[V + 1] = sum[0].den;
+#pragma unroll
+      for (int v = 0; v < V; ++v) mine[v] = sum[0].num[v];
+      // the row's warps, which left or stayed together
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WARPS), "n"(WARPS * 32) : "memory");
+      if (warp % WARPS != 0) return;
+#pragma unroll
+      for (int k = 1; k < WARPS; ++k) {
+        const float* other = part[warp + k][lane];
+        float x[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = other[v];
+        sum[0].add(other[V], other[V + 1], x);
+      }
     }
 #pragma unroll
     for (int c = 0; c < kCols; ++c)

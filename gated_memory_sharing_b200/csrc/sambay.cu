@@ -1689,6 +1689,7 @@ struct Kv4Plan {
   int nt = 1, row_tiles = 1, cols = 8, grid = 0;
   bool one_tile = false;       // no pair has more than one tile: nothing is shared
   int combine_cols = 1;        // rows that a warp of the combine kernel takes; 0: several CTAs a row
+  int combine_warps = 1;       // warps that share them
   size_t ml_part = 0, total = 0;
 };
 
@@ -1711,6 +1712,7 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   // CTAs to run at once: several CTAs a row (3 x 8191 f32: 9 us, by warps 14 us).
   const long long warps = pl.grid * static_cast<long long>(sambay::kv4::kWarps);
   const bool at_once = static_cast<long long>(d->batch) * q_heads * tokens * (d->head_dim / 32) <= 4 * kSplitTarget;
+  pl.combine_warps = warps > 6 * pairs ? 4 : 1;
   pl.combine_cols = warps <= 2 * pairs && pl.cols >= 4 ? 4 : warps > 8 * pairs && at_once ? 0 : 1;
   if (!pl.one_tile) {
     const size_t parts = static_cast<size_t>(pl.grid) * sambay::kv4::kWarps * 2 * pl.cols;
@@ -1738,13 +1740,17 @@ sambay_status kv4_attn_launch(int dev, const sambay::kv4::AttnParams& p, const K
   }
   if (!pl.one_tile) {
     auto k0 = kv4_combine_kernel<T, D, NT, 0>, k1 = kv4_combine_kernel<T, D, NT, 1>, k4 = kv4_combine_kernel<T, D, NT, 4>;
+    auto k1w4 = kv4_combine_kernel<T, D, NT, 1, 4>;
     SAMBAY_MAX_CARVEOUT(k0, dev);
     SAMBAY_MAX_CARVEOUT(k1, dev);
+    SAMBAY_MAX_CARVEOUT(k1w4, dev);
     SAMBAY_MAX_CARVEOUT(k4, dev);
-    const int cols = pl.combine_cols, pairs = p.pg.Hkv * p.row_tiles;
-    const int grid = cols == 0 ? pairs * p.cols * (D / 32) : (pairs * ((p.cols + cols - 1) / cols) + 7) / 8;
+    const int cols = pl.combine_cols, warps = pl.combine_warps, pairs = p.pg.Hkv * p.row_tiles;
+    const int grid =
+        cols == 0 ? pairs * p.cols * (D / 32) : (pairs * ((p.cols + cols - 1) / cols) * warps + 7) / 8;
     ProfScope ps("kv4_combine", st);
-    if (launch_k(cols == 0 ? k0 : cols == 1 ? k1 : k4, dim3(grid, p.pg.B), dim3(256), 0, st, true, 1, p) != cudaSuccess)
+    if (launch_k(cols == 0 ? k0 : cols == 4 ? k4 : warps == 4 ? k1w4 : k1, dim3(grid, p.pg.B), dim3(256), 0, st, true, 1,
+                 p) != cudaSuccess)
       return SAMBAY_ERR_CUDA;
   }
   return SAMBAY_OK;
