@@ -1707,12 +1707,15 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   pl.grid = static_cast<int>(std::min(static_cast<long long>(kSplitTarget) * ctas, pairs * tiles));
   pl.one_tile = tiles == 1;
   // Parts of a pair (about): few, and many rows: a warp joins 4 rows (64 x 2048
-  // tokens at 320 heads: 15 us, by single rows 22 us); more: a row (8 x 4097
-  // tokens, 4 queries: 11 us, by 4 rows 26 us); many, of rows few enough for all
-  // CTAs to run at once: several CTAs a row (3 x 8191 f32: 9 us, by warps 14 us).
+  // tokens at 320 heads: 15 us, by single rows 22 us); more: a row, or 4 warps a
+  // row while all CTAs run at once (16 x 4096 tokens, 64 heads on 8: 24.6 us the
+  // call, by one warp 30.4; 64 x 2048 at head size 128, more CTAs than that: 42.3
+  // against 37.4); many, of rows few enough: several CTAs a row (3 x 8191 f32: 9
+  // us, by warps 14 us).
   const long long warps = pl.grid * static_cast<long long>(sambay::kv4::kWarps);
-  const bool at_once = static_cast<long long>(d->batch) * q_heads * tokens * (d->head_dim / 32) <= 4 * kSplitTarget;
-  pl.combine_warps = warps > 6 * pairs ? 4 : 1;
+  const long long all_rows = static_cast<long long>(d->batch) * q_heads * tokens;
+  const bool at_once = all_rows * (d->head_dim / 32) <= 4 * kSplitTarget;
+  pl.combine_warps = warps > 3 * pairs && all_rows <= 16 * kSplitTarget ? 4 : 1;
   pl.combine_cols = warps <= 2 * pairs && pl.cols >= 4 ? 4 : warps > 8 * pairs && at_once ? 0 : 1;
   if (!pl.one_tile) {
     const size_t parts = static_cast<size_t>(pl.grid) * sambay::kv4::kWarps * 2 * pl.cols;
