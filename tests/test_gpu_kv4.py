@@ -260,6 +260,32 @@ def test_many_long_and_short_sequences(dtype, Hq, Hkv, dh, page):
         check(alone[at][j:j + 1], q[at][j:j + 1], kk[j:j + 1], vv[j:j + 1], [lens[some[j]]], what="alone")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,Hq,Hkv,dh", [
+    (150, 4, 2, 64),          # 1 or 4 warps join a row, by how many rows there are
+    (301, 2, 1, 128),
+    (600, 2, 2, 64),
+    (130, 48, 3, 64),
+])
+def test_one_long_sequence_among_many_empty(B, Hq, Hkv, dh, dtype):
+    """Rows of many parts beside rows of none, in batches of many rows."""
+    n, at = 2500, B // 2
+    lens = [n if b == at else (0, 0, 1, 0)[b % 4] for b in range(B)]
+    K, V = rows(58, 1, n, Hkv, dh, dtype=dtype), rows(59, 1, n, Hkv, dh, dtype=dtype)
+    c = make(B, Hkv, dh, n, 64, dtype)
+    c.write(K.expand(B, -1, -1, -1).contiguous(), V.expand(B, -1, -1, -1).contiguous(), i32([0] * B), i32(lens))
+    q = rows(60, B, 1, Hq, dh, dtype=dtype)
+    out = c.attend(q, i32(lens))
+    kk, vv = kv4_kept(f64(K)), kv4_kept(f64(V))
+    check(out[at:at + 1], q[at:at + 1], kk, vv, [n], what="long")
+    one = [b for b in range(B) if lens[b] == 1]
+    sel = torch.tensor(one, device="cuda")
+    rep = lambda x: np.repeat(x[:, :1], len(one), axis=0)
+    check(out[sel], q[sel], rep(kk), rep(vv), [1] * len(one), what="one token")
+    assert torch.all(out[torch.tensor([b for b in range(B) if lens[b] == 0], device="cuda")] == 0)
+    assert torch.equal(out, c.attend(q, i32(lens)))
+
+
 def test_exponents_and_scale():
     B, H, dh, lens = 2, 4, 64, [130, 77]
     Kr, Vr = rows(60, B, 130, H, dh, scale=2.0 ** -20), rows(61, B, 130, H, dh, scale=2.0 ** 13)
