@@ -563,9 +563,12 @@ constexpr long long kWaitCycles = 1LL << 31;     // a copy that has not come aft
 // Probabilities are kept times 2^15 (the largest of a row is 2^15): as f16 they
 // then have 11 bits down to 2^-29 of the largest instead of 2^-14, which shows
 // where the likeliest tokens' values are zero.  Numerator and denominator carry
-// the same factor.
+// the same factor.  The largest score is taken away before the scale is
+// multiplied in, so that the largest exponent is 15 however large the logits
+// are: with 15 - scale * largest rounded to f32 it was off by half a step of
+// that, past f16's end at 2^16 from logits of 2^24 on.
 constexpr float kPShift = 15.0f;
-constexpr float kNoRef = 3e38f;                  // the exponent offset of a row that has seen nothing
+constexpr float kNone = 3e38f;                   // less the largest score of a row that has seen nothing
 
 // Resident CTAs an SM.  The kernel is bound by what the warp schedulers can
 // dispatch, not by latency (12, 16 and 20 warps an SM measured the same), so a
@@ -580,7 +583,7 @@ struct AttnParams {
   const int32_t* lens;     // [B] cached tokens, the T new ones among them
   const int32_t* count;    // [B] query tokens of each sequence, or null (T)
   float* o_part;           // [warp][first or last pair][cols, D]  partial outputs
-  float* ml_part;          // [warp][first or last pair][cols, 2]  their (largest logit, in base 2 and less kPShift; l)
+  float* ml_part;          // [warp][first or last pair][cols, 4]  their (largest score, l, factor of the scores, -)
   int T_, Hq, G;
   int group_inv;           // ceil(2^16 / G): r * group_inv >> 16 is r / G (r < 256, G <= 16)
   int row_tiles, cols;     // cols: min(8 NT, G T) columns of a row tile
@@ -929,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
   uint32_t qb[NQ][NT][KS][2];
   float f[NT][2];
   int lim[NT][2];
-  float ref[NT][2], l[NT][2], o[NT][KS][4];
+  float low[NT][2], l[NT][2], o[NT][KS][4];    // low: less the largest score
   // where registers allow, the first queries are on their way while the first pages are looked up
   constexpr bool kEarly = !SPLIT;
   if (kEarly) fetch();
@@ -985,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
         for (int e = 0; e < 2; ++e) {
           f[n][e] = __shfl_sync(0xFFFFFFFFu, fac, (2 * t + e) * 4);
           lim[n][e] = min(c.len, __shfl_sync(0xFFFFFFFFu, limit, (2 * t + e) * 4));
-          ref[n][e] = kNoRef;
+          low[n][e] = kNone;
           l[n][e] = 0.0f;
         }
 #pragma unroll
@@ -1053,14 +1056,14 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
         }
       }
     };
-    // Online softmax per column: p = 2^(f s + ref), f > 0, ref = kPShift less the
-    // largest logit so far; mx: a lane's largest s.  Most tiles hold no larger one.
+    // Online softmax per column: p = 2^(f (s + low) + kPShift), f > 0, low = less the
+    // largest s so far; mx: a lane's largest s.  Most tiles hold no larger one.
     auto raise = [&](const float (&mx)[NT][2]) {
       bool grown = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) grown |= fmaf(mx[n][e], f[n][e], ref[n][e]) > kPShift;
+        for (int e = 0; e < 2; ++e) grown |= mx[n][e] > -low[n][e];
       if (!__any_sync(0xFFFFFFFFu, grown)) return;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -1071,9 +1074,9 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
           x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-          const float to = fminf(ref[n][e], kPShift - x * f[n][e]);
-          corr[e] = ex2_approx(to - ref[n][e]);            // 0 from kNoRef
-          ref[n][e] = to;
+          const float to = fminf(low[n][e], -x);
+          corr[e] = ex2_approx((to - low[n][e]) * f[n][e]);        // from kNone: of zeros
+          low[n][e] = to;
           l[n][e] *= corr[e];
         }
 #pragma unroll
@@ -1088,8 +1091,10 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
     auto probabilities = [&](const float (&s)[NT][4], uint32_t (&pb)[NQ][NT][2]) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float2 fn = make_float2(f[n][0], f[n][1]), rn = make_float2(ref[n][0], ref[n][1]);
-        const float2 u = fma2(make_float2(s[n][0], s[n][1]), fn, rn), v = fma2(make_float2(s[n][2], s[n][3]), fn, rn);
+        const float2 fn = make_float2(f[n][0], f[n][1]), low2 = make_float2(low[n][0], low[n][1]);
+        const float2 shift = make_float2(kPShift, kPShift);
+        const float2 u = fma2(add2(make_float2(s[n][0], s[n][1]), low2), fn, shift);
+        const float2 v = fma2(add2(make_float2(s[n][2], s[n][3]), low2), fn, shift);
         const float2 pu = make_float2(ex2_approx(u.x), ex2_approx(u.y)), pv = make_float2(ex2_approx(v.x), ex2_approx(v.y));
         const float2 ln = add2(make_float2(l[n][0], l[n][1]), add2(pu, pv));
         l[n][0] = ln.x;
@@ -1312,7 +1317,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
               float* dst = p.o_part + (slot * p.cols + col) * D;
 #pragma unroll
               for (int k = 0; k < KS; ++k) store2(dst + 16 * k + 2 * g, o[n][k][e], o[n][k][e + 2]);
-              if (g == 0) store2(p.ml_part + (slot * p.cols + col) * 2, -ref[n][e], ls);
+              if (g == 0)
+                *reinterpret_cast<float4*>(p.ml_part + (slot * p.cols + col) * 4) = make_float4(-low[n][e], ls, f[n][e], 0.0f);
             }
           }
         }
@@ -1323,16 +1329,17 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
   }
 }
 
-// A running sum of parts of one row: values relative to 2^m, and what they are to be divided by.
+// A running sum of parts of one row: values relative to 2^(f m), f the row's
+// factor, and what they are to be divided by.
 template <int V>
 struct RowSum {
-  float m = -kNoRef, den = 0.0f, num[V] = {};
-  __device__ __forceinline__ void add(float m2, float den2, const float (&x)[V]) {
-    const float to = fmaxf(m, m2), f = ex2_approx(m - to), f2 = ex2_approx(m2 - to);
-    m = to;
-    den = den * f + den2 * f2;
+  float m = -kNone, den = 0.0f, num[V] = {};
+  __device__ __forceinline__ void add(float f, float m2, float den2, const float (&x)[V]) {
+    const float d = (m2 - m) * f, c = ex2_approx(fminf(-d, 0.0f)), c2 = ex2_approx(fminf(d, 0.0f));
+    m = fmaxf(m, m2);
+    den = den * c + den2 * c2;
 #pragma unroll
-    for (int v = 0; v < V; ++v) num[v] = num[v] * f + x[v] * f2;
+    for (int v = 0; v < V; ++v) num[v] = num[v] * c + x[v] * c2;
   }
 };
 
@@ -1380,19 +1387,23 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
     for (int v = 0; v < V; v += 2) store2(dst + v, sum.num[v] * inv, sum.num[v + 1] * inv);
   };
   const int r0 = rt * (8 * NT) + col0;
+  auto part_of = [&](long long k) { return *reinterpret_cast<const float2*>(p.ml_part + k * 4); };
+  auto factor_of = [&](long long k) { return p.ml_part[k * 4 + 2]; };
   if (!MANY) {
     RowSum<V> sum[kCols];
+    float f[kCols] = {};
 #pragma unroll kCols == 1 ? 4 : 2
     for (int w = w0 + warp % WARPS; w <= w1; w += WARPS) {
       const long long k = (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col0;
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
         if (r0 + c < rows && col0 + c < p.cols) {
-          const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + (k + c) * 2);
+          const float2 ml = part_of(k + c);
+          f[c] = factor_of(k + c);
           float x[V];
 #pragma unroll
           for (int v = 0; v < V; v += 2) load2(p.o_part + (k + c) * D + at + v, x + v);
-          sum[c].add(ml.x, ml.y, x);
+          sum[c].add(f[c], ml.x, ml.y, x);
         }
     }
     if constexpr (WARPS > 1) {
@@ -1412,7 +1423,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
         float x[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) x[v] = other[v];
-        sum[0].add(other[V], other[V + 1], x);
+        sum[0].add(f[0], other[V], other[V + 1], x);
       }
     }
 #pragma unroll
@@ -1422,14 +1433,15 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
   }
   if (r0 >= rows) return;              // the whole CTA's
   RowSum<V> sum;
+  const float f = factor_of((static_cast<long long>(w0) * 2 + first) * p.cols + col0);
 #pragma unroll 4
   for (int w = w0 + (threadIdx.x >> 3); w <= w1; w += 32) {
     const long long k = (static_cast<long long>(w) * 2 + (w == w0 ? first : 0)) * p.cols + col0;
-    const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + k * 2);
+    const float2 ml = part_of(k);
     float x[V];
 #pragma unroll
     for (int v = 0; v < V; v += 2) load2(p.o_part + k * D + at + v, x + v);
-    sum.add(ml.x, ml.y, x);
+    sum.add(f, ml.x, ml.y, x);
   }
   // the four of a warp, then the warps
 #pragma unroll
@@ -1437,7 +1449,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
     float x[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) x[v] = __shfl_xor_sync(0xFFFFFFFFu, sum.num[v], o);
-    sum.add(__shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.den, o), x);
+    sum.add(f, __shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.den, o), x);
   }
   __shared__ float sh[8][8][V + 2];
   if (lane < 8) {
@@ -1455,7 +1467,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnParams p) {
     float x[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) x[v] = other[v];
-    sum.add(other[V], other[V + 1], x);
+    sum.add(f, other[V], other[V + 1], x);
   }
   store(sum, r0);
 }

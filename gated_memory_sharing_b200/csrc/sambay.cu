@@ -1720,7 +1720,7 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   if (!pl.one_tile) {
     const size_t parts = static_cast<size_t>(pl.grid) * sambay::kv4::kWarps * 2 * pl.cols;
     pl.ml_part = round256(parts * d->head_dim * 4);
-    pl.total = pl.ml_part + round256(parts * 2 * 4);
+    pl.total = pl.ml_part + round256(parts * 4 * 4);
   }
   return pl;
 }

@@ -471,8 +471,9 @@ SAMBAY_API sambay_status sambay_kv4_read(const sambay_kv4_cache* cache, const sa
  * Products are float32 accumulations of f16 operands: what the cache holds is
  * exact in f16, q is scaled per row by a power of two, and the probabilities
  * are rounded to f16 (SAMBAY_F32: q and the probabilities are split into pairs
- * of f16, 22 bits).  A value that is NaN reaches only the queries that see its
- * token.  Results do not vary from run to run (parts are joined in a fixed
+ * of f16, 22 bits).  The largest score is taken away before the scale is
+ * multiplied in, so logits may be as large as they get.  A value that is NaN
+ * reaches only the queries that see its token.  Results do not vary from run to run (parts are joined in a fixed
  * order); how the work is cut depends on all sequences' lengths, so a sequence's
  * last bits may differ with the batch it is in.
  */

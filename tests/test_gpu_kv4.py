@@ -311,6 +311,53 @@ def test_dominant_and_equal_logits():
     check(c.attend(q, i32([500])), q, K, V, [500], what="logits far apart and equal")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 16, 2), (2, 16, 1)])       # 8 columns; 16, and two tiles of rows
+@pytest.mark.parametrize("keys", ["top", "least negative", "equal"])
+def test_large_logits(keys, T, Hq, Hkv, dh, dtype):
+    """Logits (in base 2) of 2^20 to 2^101: one key above the others, whose value
+    is the output, or all keys the same, whose mean value it is.
+
+    Rows of keys are +-1, +-.25 or +-2 (kept as 1.03125 times that), and queries
+    have the signs of the top key: the other logits are at least 3/4 of the top
+    one's size below it.  Both may be off by dh + 4 roundings of 2^-23, below 2^-15
+    of their size, so the others weigh less than 2^-100 from 2^20 on, and the bound
+    has no part of the logits' errors.  Equal keys give equal sums, whatever they
+    are off by."""
+    lens = [2, 33, 700, 5000]                   # one tile; several; pairs that several warps share
+    B, n = len(lens), max(lens)
+    g = torch.Generator("cuda").manual_seed(dh + T)
+    signs = lambda *shape: 2.0 * torch.randint(0, 2, shape, generator=g, device="cuda") - 1.0  # noqa: E731
+    u = signs(1, 1, Hkv, dh)
+    at = [0, 20, 123, 3456]
+    K = {"top": 0.25 * signs(B, n, Hkv, dh), "least negative": -2.0 * u.expand(B, n, -1, -1),
+         "equal": u.expand(B, n, -1, -1)}[keys].to(dtype).contiguous()
+    for b, j in enumerate(at):
+        if keys != "equal":
+            K[b, j] = (u if keys == "top" else -u)[0, 0].to(dtype)
+    V = rows(73, B, n, Hkv, dh, dtype=dtype)
+    c = make(B, Hkv, dh, n, 64, dtype)
+    c.write(K, V, i32([0] * B), i32(lens))
+    kept = np.repeat(kv4_kept(f64(V)), Hq // Hkv, axis=2)                    # [B, n, Hq, dh]
+    want, spread = np.zeros((B, T, Hq, dh)), np.zeros((B, T, Hq, dh))
+    for b, j in enumerate(at):
+        for t in range(T):
+            seen = slice(0, lens[b] - (T - 1 - t)) if keys == "equal" else slice(j, j + 1)
+            want[b, t], spread[b, t] = kept[b, seen].mean(0), np.abs(kept[b, seen]).mean(0)
+    lim = bound(want, spread, np.zeros((B, T, Hq)), dtype, dh, n)
+    wrong = {}
+    for log2 in (20, 24, 25, 26, 27, 28, 30, 45, 60, 100):
+        for scale in (None, 1e4):
+            size = 2.0 ** log2 * np.log(2.0) / (dh * (scale or dh ** -0.5))
+            q = size * (1 + torch.rand(B, T, Hq, dh, generator=g, device="cuda", dtype=torch.float64))
+            q = (q.view(B, T, Hkv, -1, dh) * u[:, :, :, None].double()).view(B, T, Hq, dh).to(dtype)
+            off = (np.abs(f64(c.attend(q, i32(lens), scale=scale or 0.0)) - want) / lim).max(-1)
+            if not np.all(off <= 1.0):
+                wrong[log2, scale] = np.mean(~(off <= 1.0))
+    assert not wrong, f"shares of rows that are off, by log2 of the logits and scale: {wrong}"
+
+
 def test_what_is_not_the_sequences_is_not_read():
     """NaN in every byte behind the last token, in the spare pages, and in another sequence's tokens."""
     for dh, n in ((64, 50), (128, 17)):
