@@ -397,7 +397,9 @@ class KV4Cache:
             return (_current_stream(self._dev),
                     None if _current_device() == self._dev else torch.cuda.device(self._dev))
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device)
+            # (torch takes the handle 0 as a wish for a stream of its pool)
+            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream
+                      else torch.cuda.default_stream(self.device))
         if stream.device != self.device:
             raise ValueError(f"a stream of {stream.device} for a cache on {self.device}")
         return stream.cuda_stream, torch.cuda.stream(stream)

@@ -527,6 +527,25 @@ def test_streams_and_graphs():
         assert same(f64(c.read(pos, 1)[0]), kv4_kept(f64(x)))
 
 
+def test_the_default_stream_by_its_handle():
+    """The handle 0 is the default stream's: calls given it follow what was queued there."""
+    assert torch.cuda.default_stream().cuda_stream == 0
+    lens = [200, 77]
+    c, _, _ = filled(2, 4, 64, 16, lens, BF16, seed=185)
+    n, pos = i32(lens), i32([199, 76])
+    src, xs = rows(186, 2, 1, 8, 64), rows(187, 2, 1, 4, 64)
+    assert c._on(0)[0] == 0
+    x, q = torch.zeros_like(xs), torch.zeros_like(src)
+    torch.cuda._sleep(20_000_000)              # about 10 ms in front of the copies
+    x.copy_(xs)
+    q.copy_(src)
+    c.write(x, x, pos, stream=0)
+    out = c.attend(q, n, stream=torch.cuda.default_stream().cuda_stream)
+    Ko, _ = c.read(pos, 1, stream=0)
+    assert same(f64(Ko), kv4_kept(f64(xs)))
+    assert torch.equal(out, c.attend(src, n))
+
+
 def test_after_other_work_in_a_graph():
     """Captured behind a copy, a fill, and a join with another stream: each call still follows what was queued before it."""
     lens = [200, 77]
