@@ -353,9 +353,13 @@ class KV4Cache:
 
     @staticmethod
     def exponents(rows) -> torch.Tensor:
-        """[Hkv] int32 for rows [..., Hkv, dh]: the least e for which the
-        largest of these values is not past what a block can hold, 2688 * 2^e."""
-        amax = rows.detach().abs().amax(-1).reshape(-1, rows.shape[-2]).amax(0).double()
+        """[Hkv] int32 for rows [..., Hkv, dh]: the least e in -64 .. 64 for
+        which the largest of these values is not past what a block can hold,
+        2688 * 2^e.  Infinities and NaN do not count: they take their own block
+        of 16 values only, not their head."""
+        size = rows.detach().abs()
+        size = torch.where(torch.isfinite(size), size, 0)
+        amax = size.amax(-1).reshape(-1, rows.shape[-2]).amax(0).double()
         e = torch.ceil(torch.log2(torch.clamp(amax, min=2.0 ** -60) / 2688.0))
         return torch.clamp(e, -64, 64).to(torch.int32)
 

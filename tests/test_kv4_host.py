@@ -2,8 +2,10 @@
 case is built so that validation fails before the library touches a device."""
 
 import pytest
+import torch
 
 from gated_memory_sharing_b200 import abi, build
+from gated_memory_sharing_b200.layers import KV4Cache
 
 
 class _Ptr:
@@ -124,3 +126,18 @@ def test_attention_refusals():
     refused(3, fn, cache(), d, 8, 1, Q, OUT, LENS, None, 0.0, None)
     refused(3, fn, cache(), d, 8, 1, Q, OUT, LENS, None, 0.0, _Ptr(0xA0000, need - 1))
     refused(3, fn, cache(), d, 8, 1, Q, OUT, LENS, None, 0.0, _Ptr(0xA0010, need))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_exponents_of_rows_with_infinities_and_nan(dtype):
+    x = torch.zeros(3, 5, 4, 64, dtype=dtype)
+    x[1, 2, 0, 7], x[0, 0, 1, 0], x[2, 4, 2, 63] = 2688.0, -2689.0 - 11, 2.0 ** -9     # bf16: 2704
+    want = torch.tensor([0, 1, -20, -64], dtype=torch.int32)
+    assert torch.equal(KV4Cache.exponents(x), want)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        y = x.clone()
+        y[0, 1, :, 5] = bad                     # one in every head
+        assert torch.equal(KV4Cache.exponents(y), want)
+    # nothing but these, and past what an exponent of 64 holds
+    assert torch.equal(KV4Cache.exponents(torch.full((2, 1, 16), float("nan"), dtype=dtype)), torch.tensor([-64], dtype=torch.int32))
+    assert KV4Cache.exponents(torch.full((2, 1, 16), 3e38, dtype=dtype)).item() == 64
