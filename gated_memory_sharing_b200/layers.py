@@ -306,7 +306,8 @@ class KV4Cache:
     each sequence has its own pages, in order).  The table may be changed in
     place between calls, on the stream of the calls.  ``k_exp`` / ``v_exp``
     [Hkv] int32: the power of two of each head's rows (see :meth:`exponents`),
-    fixed for the cache's life.
+    fixed for the cache's life.  These tensors and ``pages`` are the cache's own
+    (calls use their addresses): another one cannot be put in their place.
 
     Positions, lengths and counts are int32 tensors on the device.  Indices
     outside the table, the pool or a call's rows are skipped and recorded
@@ -333,7 +334,7 @@ class KV4Cache:
         self._dev = self.device.index
         self.io, self.dtype = io, io_dtype(io)
         self.batch, self.kv_heads, self.head_dim, self.page_tokens = batch, kv_heads, head_dim, page_tokens
-        self.table, self.k_exp, self.v_exp = table, k_exp, v_exp
+        self._own = {"table": table, "k_exp": k_exp, "v_exp": v_exp}
         if table.dim() != 2 or table.shape[0] != batch:
             raise ValueError(f"table is [{batch}, pages]: got {tuple(table.shape)}")
         self._index(table, "table", None)
@@ -347,9 +348,18 @@ class KV4Cache:
                              "at most 2^30 tokens a sequence")
         with torch.cuda.device(self.device):
             # zeros: a page that was never written reads as zeros
-            self.pages = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self._own["pages"] = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.abi_cache = abi.make_kv4_cache(self.pages, table, k_exp, v_exp)
         self._plans, self._row_shapes = {}, set()
+
+    def _fixed(name):
+        def put(self, t):
+            if t is not self._own[name]:                 # `cache.table += 1` puts the same tensor back
+                raise ValueError(f"{name} belongs to the cache: change it in place")
+        return property(lambda self: self._own[name], put)
+
+    table, k_exp, v_exp, pages = map(_fixed, ("table", "k_exp", "v_exp", "pages"))
+    del _fixed
 
     @staticmethod
     def exponents(rows) -> torch.Tensor:

@@ -578,6 +578,27 @@ def test_after_other_work_in_a_graph():
         assert torch.equal(out, wants[k]) and same(f64(Ko), kv4_kept(f64(xs)))
 
 
+def test_the_table_changes_in_place_only():
+    lens = [100, 60]
+    c, K, V = filled(2, 2, 64, 16, lens, BF16, seed=175)
+    q = rows(176, 2, 1, 4, 64)
+    want = c.attend(q, i32(lens))
+    moved = c.table.clone()
+    moved[0, 0], moved[0, 1] = c.table[0, 1], c.table[0, 0]        # 16 tokens before the 16 in front of them
+    with pytest.raises(ValueError):
+        c.table = moved
+    assert torch.equal(c.attend(q, i32(lens)), want)
+    table = c.table
+    c.table += 0
+    c.table[:] = moved
+    assert c.table is table
+    for x in (K, V):
+        x[0, :32] = np.concatenate([x[0, 16:32], x[0, :16]])
+    check(c.attend(q, i32(lens)), q, K, V, lens, what="pages exchanged")
+    Ko, Vo = c.read(i32([0, 0]), 60)
+    assert same(f64(Ko), K[:, :60]) and same(f64(Vo), V[:, :60])
+
+
 def test_layer_refusals():
     c = KV4Cache(2, 4, 64, 100, page_tokens=16)
     k = rows(180, 2, 5, 4, 64)

@@ -141,3 +141,18 @@ def test_exponents_of_rows_with_infinities_and_nan(dtype):
     # nothing but these, and past what an exponent of 64 holds
     assert torch.equal(KV4Cache.exponents(torch.full((2, 1, 16), float("nan"), dtype=dtype)), torch.tensor([-64], dtype=torch.int32))
     assert KV4Cache.exponents(torch.full((2, 1, 16), 3e38, dtype=dtype)).item() == 64
+
+
+@pytest.mark.parametrize("name", ["table", "k_exp", "v_exp", "pages"])
+def test_the_layers_tensors_cannot_be_exchanged(name):
+    """Calls use the addresses that the cache was made with: a new tensor in its place would not be seen."""
+    c = KV4Cache.__new__(KV4Cache)
+    old = torch.zeros(4, dtype=torch.int32)
+    c._own = {name: old}
+    with pytest.raises(ValueError):
+        setattr(c, name, old.clone())
+    with pytest.raises(ValueError):
+        setattr(c, name, None)
+    assert getattr(c, name) is old
+    setattr(c, name, old.add_(1))               # what an operation in place does
+    assert getattr(c, name) is old and old[0] == 1
