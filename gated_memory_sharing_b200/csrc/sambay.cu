@@ -1679,6 +1679,12 @@ sambay_status kv4_rows(bool write, const sambay_kv4_cache* c, const sambay_kv4_d
   return d->head_dim == 64 ? kv4_rows_launch<T, 64>(write, p, st) : kv4_rows_launch<T, 128>(write, p, st);
 }
 
+// Whether two arrays of n elements of the cache's io type share memory.
+bool kv4_overlap(const void* a, const void* b, size_t n, int32_t io) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x < y ? y - x : x - y) < n * io_bytes(io);
+}
+
 constexpr int kKv4MaxTokens = 16;
 
 // The attention's grid, for a 148-SM B200 (a function of the sizes only, so
@@ -1814,7 +1820,9 @@ sambay_status sambay_kv4_read(const sambay_kv4_cache* c, const sambay_kv4_dims* 
   SAMBAY_TRY(check_ptrs({K, V}));
   SAMBAY_TRY(kv4_check_index(pos, false));
   SAMBAY_TRY(kv4_check_index(count, true));
-  if (K == V || K == c->pages || V == c->pages) return SAMBAY_ERR_INVALID_ARG;
+  if (K == c->pages || V == c->pages) return SAMBAY_ERR_INVALID_ARG;
+  if (kv4_overlap(K, V, static_cast<size_t>(d->batch) * tokens * d->kv_heads * d->head_dim, d->io))
+    return SAMBAY_ERR_INVALID_ARG;
   int dev, sms;
   SAMBAY_TRY(current_device(&dev, &sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -1836,7 +1844,9 @@ sambay_status sambay_cross_attn_decode_kv4(const sambay_kv4_cache* c, const samb
   SAMBAY_TRY(check_ptrs({q, out}));
   SAMBAY_TRY(kv4_check_index(lens, false));
   SAMBAY_TRY(kv4_check_index(count, true));
-  if (out == q || out == c->pages || q == c->pages) return SAMBAY_ERR_INVALID_ARG;
+  if (out == c->pages || q == c->pages) return SAMBAY_ERR_INVALID_ARG;
+  if (kv4_overlap(out, q, static_cast<size_t>(d->batch) * tokens * q_heads * d->head_dim, d->io))
+    return SAMBAY_ERR_INVALID_ARG;
   if (!(scale >= 0.0f) || scale > 1e4f) return SAMBAY_ERR_INVALID_ARG;   // also rejects NaN
   const Kv4Plan pl = kv4_plan(d, q_heads, tokens);
   SAMBAY_TRY(check_ws(ws, ws_bytes, pl.total));

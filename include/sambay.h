@@ -445,8 +445,8 @@ SAMBAY_API sambay_status sambay_kv4_write(const sambay_kv4_cache* cache, const s
 
 /*
  * sambay_kv4_read - the values that positions pos[b] .. pos[b] + count[b] - 1
- * stand for, as rows: K, V [B, tokens, Hkv, dh] io out, dense.  Rows from
- * count[b] on are left as they were.
+ * stand for, as rows: K, V [B, tokens, Hkv, dh] io out, dense, which share no
+ * memory.  Rows from count[b] on are left as they were.
  */
 SAMBAY_API sambay_status sambay_kv4_read(const sambay_kv4_cache* cache, const sambay_kv4_dims* dims,
                                          int32_t tokens, void* K, void* V, const int32_t* pos,
@@ -461,7 +461,7 @@ SAMBAY_API sambay_status sambay_kv4_read(const sambay_kv4_cache* cache, const sa
  * (with tokens = 1, all of it).  A query that sees no token gives 0; rows of
  * out from n on are left as they were.
  *
- *   q, out [B, tokens, Hq, dh] io (out must not alias q); Hq a multiple of Hkv,
+ *   q, out [B, tokens, Hq, dh] io (they share no memory); Hq a multiple of Hkv,
  *   G = Hq / Hkv <= 16;  1 <= tokens <= 16;  lens [B] int32;  scale > 0, or 0
  *   for 1 / sqrt(dh).
  *   ws: >= sambay_cross_attn_decode_kv4_workspace(dims, q_heads, tokens); no

@@ -156,3 +156,20 @@ def test_the_layers_tensors_cannot_be_exchanged(name):
     assert getattr(c, name) is old
     setattr(c, name, old.add_(1))               # what an operation in place does
     assert getattr(c, name) is old and old[0] == 1
+
+
+def test_outputs_that_share_memory_with_other_rows():
+    """Not only the same address: any byte in common.  (Where they have none, a short workspace keeps the call from a launch.)"""
+    d = dims(table_pages=64)
+    n = 2 * 3 * 4 * 64 * 2                       # bytes of K and of V, 3 tokens
+    for io, size in ((abi.BF16, n), (abi.F32, 2 * n)):
+        d.io = io
+        for off in (0, 16, size - 16, -16, 16 - size):
+            refused(1, abi.sambay_kv4_read, cache(), d, 3, K, _Ptr(K.address + off), POS)
+    d.io = abi.BF16
+    need = abi.sambay_cross_attn_decode_kv4_workspace(d, 8, 3)
+    short, n = _Ptr(0xA0000, need - 1), 2 * n    # 8 query heads
+    for off in (0, 16, n - 16, -16, 16 - n):
+        refused(1, abi.sambay_cross_attn_decode_kv4, cache(), d, 8, 3, Q, _Ptr(Q.address + off), LENS, None, 0.0, short)
+    for off in (n, -n):                          # one behind the other: the next check's turn
+        refused(3, abi.sambay_cross_attn_decode_kv4, cache(), d, 8, 3, Q, _Ptr(Q.address + off), LENS, None, 0.0, short)
