@@ -261,6 +261,59 @@ def test_many_long_and_short_sequences(dtype, Hq, Hkv, dh, page):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("G,T,Hkv", [
+    (5, 1, 8),       # 8 columns: 4 rows and one more
+    (7, 1, 8),       # ... and three more
+    (11, 1, 5),      # 16 columns, three more than 8
+    (5, 2, 5),       # rows of two tokens, 10 in all
+    (7, 3, 3),       # two tiles of rows, 16 and 5
+    (1, 4, 8),       # just 4
+])
+def test_rows_joined_four_at_a_time(G, T, Hkv, dh, dtype):
+    """Many pairs of few parts each, the last columns of a pair among them."""
+    rows_, B = G * T, 126
+    lens = [(0, 3, 900, 64, 333, 128, 1, 517, 250)[i % 9] + i for i in range(B)]
+    tiles, wide = -(-rows_ // (8 if rows_ <= 8 else 16)), 8 if rows_ <= 8 else 16
+    pairs, warps = B * Hkv * tiles, 4 * 148 * (3 if wide == 8 else 2)
+    assert warps <= 2 * pairs and min(rows_, wide) >= 4          # this form's condition
+    K, V = rows(61, B, max(lens), Hkv, dh, dtype=dtype), rows(62, B, max(lens), Hkv, dh, dtype=dtype)
+    c = make(B, Hkv, dh, max(lens), 64, dtype)
+    c.write(K, V, i32([0] * B), i32(lens))
+    q = rows(63, B, T, Hkv * G, dh, dtype=dtype)
+    out = torch.full_like(q, 7.0)
+    counts = [T - (i % 5 == 4) for i in range(B)]
+    c.attend(q, i32(lens), i32(counts), out=out)
+    some = [0, 1, 2, 4, 7, 11, 65, 101, 120, 125]
+    at = torch.tensor(some, device="cuda")
+    check(out[at], q[at], kv4_kept(f64(K[at])), kv4_kept(f64(V[at])), [lens[i] for i in some],
+          [counts[i] for i in some], what=f"G{G} T{T}")
+    assert torch.isfinite(out).all()
+    for i, n in enumerate(counts):
+        assert torch.all(out[i, n:] == 7.0)
+    again = torch.full_like(q, 7.0)
+    assert torch.equal(out, c.attend(q, i32(lens), i32(counts), out=again))
+
+
+def test_many_sequences():
+    """More sequences than a warp's lanes have looked through so far, up to the most that a call takes."""
+    for B, n, page in ((5000, 200, 32), (65535, 80, 16)):
+        lens = np.random.default_rng(B).integers(0, n + 1, B)
+        lens[B // 2], lens[-1] = n, n
+        K, V = rows(64, B, n, 1, 64), rows(65, B, n, 1, 64)
+        c = make(B, 1, 64, n, page)
+        L = torch.from_numpy(lens.astype(np.int32)).cuda()
+        c.write(K, V, torch.zeros_like(L), L)
+        q = rows(66, B, 1, 2, 64)
+        out = c.attend(q, L)
+        some = [0, 1, 31, 32, 2047, 2048, B // 2, B - 2, B - 1] + list(range(100, B, B // 13))
+        at = torch.tensor(some, device="cuda")
+        check(out[at], q[at], kv4_kept(f64(K[at])), kv4_kept(f64(V[at])), [int(lens[i]) for i in some], what=f"B{B}")
+        assert torch.isfinite(out).all() and torch.all(out[L == 0] == 0) and torch.all(out[L > 0].abs().amax((1, 2, 3)) > 0)
+        del K, V, c, out
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("B,Hq,Hkv,dh", [
     (150, 4, 2, 64),          # 1 or 4 warps join a row, by how many rows there are
     (301, 2, 1, 128),
