@@ -573,7 +573,7 @@ constexpr float kNone = 3e38f;                   // less the largest score of a 
 // Resident CTAs an SM.  The kernel is bound by what the warp schedulers can
 // dispatch, not by latency (12, 16 and 20 warps an SM measured the same), so a
 // variant gets the registers that it needs: 168 a thread for 8 columns, 255 for
-// 16 (168 spill: 64 x 2048 tokens at 16 query heads a KV head 82 us, 255 64 us).
+// 16 (168 spill: 64 x 2048 tokens at 16 query heads a KV head 82 us, 255 67 us).
 __host__ __device__ constexpr int attn_ctas(int nt) { return nt == 1 ? 3 : 2; }
 
 struct AttnParams {
@@ -823,9 +823,9 @@ __device__ __forceinline__ void prefetch_part(const void* p, long long bytes) {
 // tokens of 64 values, 32 conversions of codes (2 clocks each), 32 multiplies by
 // scales (1.4), 8 MMAs (3.4) and the softmax, about 190 clocks of the 198 that
 // the bytes take at 6.56 TB/s.  Measured (a captured pass, the combine kernel in
-// it): 16 sequences x 34816 tokens 143 us, 5.6 TB/s, 0.86 of the copy bandwidth
-// (without its loads 133 us, without its arithmetic 125 us); 64 x 2048 43 us,
-// 4.4 TB/s, of which about 13 us are starting (lengths, table, first tiles one
+// it): 16 sequences x 34816 tokens 141 us, 5.7 TB/s, 0.87 of the copy bandwidth
+// (without its loads 133 us, without its arithmetic 125 us); 64 x 2048 44 us,
+// 4.3 TB/s, of which about 13 us are starting (lengths, table, first tiles one
 // after the other), the last parts and the combine kernel.
 //
 // Query row r of a (sequence, KV head): token r / G, head r % G of the group.
@@ -1142,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
       }
     };
     // A tile that every column sees all of.  (f32 at head size 128 would spill
-    // here, and takes all tiles by groups: 16 x 4096 tokens, 128 heads on 8, 48 us, 64 us so.)
+    // here, and takes all tiles by groups: 16 x 4096 tokens, 128 heads on 8, 50 us, 64 us so.)
     constexpr bool kWhole = !(SPLIT && D == 128);
     auto whole_tile = [&](const uint8_t* base) {
       // Its scales, 8 of K or V (`first`) converted a lane: every lane needs 1/4
@@ -1345,7 +1345,10 @@ struct RowSum {
 
 // Rows whose pair was shared by several warps, from their parts in the line's
 // order.  Grid y: sequences.  A few us, nearly all of it latency (its launch
-// overlaps the attention's end, its lengths are read before that).
+// overlaps the attention's end, its lengths are read before that), for batches of
+// up to some hundreds: every warp sums the lengths of all sequences, which grows
+// with the batch squared (100 tokens of one head, with the attention: 256
+// sequences 9.4 us, 1024 28 us, 4096 110 us, 65535 15 ms).
 //   COLS > 0: WARPS warps (each every WARPS-th part) for COLS columns of a pair,
 //   D / 32 values a lane.
 //   COLS = 0: a CTA for 32 values of a row; 8 lanes take 4 values each, 32 of

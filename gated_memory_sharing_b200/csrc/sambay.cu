@@ -383,7 +383,12 @@ struct Operand {
 // library's kernels.  Such a kernel may start (set-up, CTA launch) while its
 // predecessor finishes; each kernel waits for its predecessor (pdl_wait)
 // before touching global memory.  The first kernel of a call is launched
-// plainly and so orders after whatever the caller queued before.
+// plainly and so orders after whatever the caller queued before, but for the
+// 4-bit cache's calls: their first kernels are chained too, behind whatever was
+// queued, so before pdl_wait they may prefetch to L2 and nothing else.  A kernel
+// behind them may read before its own pdl_wait what the call does not write (the
+// joining kernel reads lengths and counts so), only because the attention's own
+// pdl_wait comes before its pdl_launch_dependents.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                      bool chained, int cluster, Args... args) {
@@ -1713,11 +1718,11 @@ Kv4Plan kv4_plan(const sambay_kv4_dims* d, int32_t q_heads, int32_t tokens) {
   pl.grid = static_cast<int>(std::min(static_cast<long long>(kSplitTarget) * ctas, pairs * tiles));
   pl.one_tile = tiles == 1;
   // Parts of a pair (about): few, and many rows: a warp joins 4 rows (64 x 2048
-  // tokens at 320 heads: 15 us, by single rows 22 us); more: a row, or 4 warps a
-  // row while all CTAs run at once (16 x 4096 tokens, 64 heads on 8: 24.6 us the
-  // call, by one warp 30.4; 64 x 2048 at head size 128, more CTAs than that: 42.3
-  // against 37.4); many, of rows few enough: several CTAs a row (3 x 8191 f32: 9
-  // us, by warps 14 us).
+  // tokens at 320 heads: 66.5 us the call, by single rows 74.2); more: a row, or 4
+  // warps a row while all CTAs run at once (16 x 4096 tokens, 64 heads on 8: 24.2
+  // us, by one warp 28.4; 64 x 2048 at head size 128, more CTAs than that: 42.5
+  // against 37.5); many, of rows few enough: several CTAs a row (3 x 8191 f32:
+  // 11.9 us, by four warps 31.5).
   const long long warps = pl.grid * static_cast<long long>(sambay::kv4::kWarps);
   const long long all_rows = static_cast<long long>(d->batch) * q_heads * tokens;
   const bool at_once = all_rows * (d->head_dim / 32) <= 4 * kSplitTarget;
