@@ -721,8 +721,9 @@ struct Cursor {
 };
 
 // n tiles on (no further than the pair's end); true if that is another pair.
-template <int D>
-__device__ __forceinline__ bool advance(const AttnParams& p, Cursor& c, int n) {
+// len: the length of a sequence that is reached.
+template <int D, typename Len>
+__device__ __forceinline__ bool advance(const AttnParams& p, Cursor& c, int n, Len len) {
   if ((c.tile += n) < c.tiles) return false;
   c.tile = 0;
   if (++c.rt == p.row_tiles) {
@@ -730,7 +731,7 @@ __device__ __forceinline__ bool advance(const AttnParams& p, Cursor& c, int n) {
     if (++c.h == p.pg.Hkv) {
       c.h = 0;
       if (++c.b < p.pg.B) {
-        c.len = len_of(p, c.b, false);
+        c.len = len(c.b);
         c.tiles = tiles_of<D>(c.len);
       }
     }
@@ -759,7 +760,8 @@ __device__ __forceinline__ int scan(int v) {
 // sequences; then the sequences of the lane that holds the place are looked
 // through.  *gap: the line's.  (Lengths must not change while a call runs; if
 // they do, what is computed is undefined, but stays inside the arrays: here, in
-// pair_left() and in the combine kernel.)
+// pair_left() and in the combine kernel; and every copy is waited for, since the
+// cursor that works takes the lengths that the one that loads has read.)
 template <int D>
 __device__ __forceinline__ int begin_of(const AttnParams& p, int gw, Cursor& c, int* gap) {
   const int lane = threadIdx.x & 31;
@@ -874,12 +876,14 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
   bool window = true;                  // to be loaded
   uint32_t have = 0;                   // SG bits a stage: which groups were loaded
   int to_load = left;                  // ... to be asked for
+  int next_len = 0;                    // of the sequence that was loaded from last
   // The tiles that a stage takes at a place: two of one pair, from an even one on.
   auto step_of = [&](const Cursor& x, int units) {
     return (x.tile & 1) ? 1 : min(min(kStageTiles, units), x.tiles - x.tile);
   };
   auto issue = [&](int st) {
     const int n = step_of(in, to_load);
+    next_len = in.len;
     const int tok = in.tile * TILE + lane * kGroup;
     if (window || in.tile % WIN == 0) {
       window = false;
@@ -905,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
     if (piece && (lane & p.piece_low) == 0)
       bulk_load(ring_addr + st * kStageBytes + lane * Block<D>::kBytes, src, __popc(piece) * Block<D>::kBytes, bar);
     have = (have & ~(((1u << SG) - 1) << (SG * st))) | mask << (SG * st);
-    window = advance<D>(p, in, n);
+    window = advance<D>(p, in, n, [&](int b) { return len_of(p, b, false); });
     to_load = window ? pair_left(p, in, to_load, n + gap) : to_load - n;
   };
   // The queries of a pair, as they lie there: column g's values 16 b + 4 t .. + 3.
@@ -1324,7 +1328,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) kv4_attn_kernel(const
         }
       fresh = true;
     }
-    left = advance<D>(p, c, n) ? pair_left(p, c, left, n + gap) : left - n;
+    left = advance<D>(p, c, n, [&](int) { return next_len; }) ? pair_left(p, c, left, n + gap) : left - n;
     i += n;
   }
 }
